@@ -530,6 +530,114 @@ ss24_status ss24_sparse_gemm_fp8(const uint8_t *a_values, const uint8_t *a_meta,
                                  const uint8_t *b, const float *b_scale, int64_t m, int64_t n, int64_t k, float *y,
                                  void *ws, size_t ws_bytes, ss24_stream stream);
 
+/* ---- serving in 8 bits: the INT8 product, a paged cache, attention over it ---- */
+
+/* Y = diag(s_a) A B^T diag(s_b) on the INT8 tensor cores: the consumer of INT8
+ * with one scale per row (§3) on both sides. a: token rows, int8 [m][k] with
+ * a_scale fp32 [m]; b: channel rows (a weight), int8 [n][k] with b_scale fp32
+ * [n]; both as ss24_quantize_int or ss24_quantize_int_rows write them (bits 8,
+ * group 0), k contiguous, packed. y (y_dtype SS24_BF16 or SS24_F32, row stride
+ * ldy >= n elements, element aligned) receives
+ *   y[t][c] = RN(RN(RN(sum_k a[t][k] b[c][k]) a_scale[t]) b_scale[c]),
+ * the sum exact in 32-bit integers for every int8 code, each RN to binary32,
+ * and one more rounding to bf16 for SS24_BF16. Elements of y beyond column n
+ * are left as they were. m, n >= 0 (zero: nothing is launched), any size; k a
+ * multiple of 16, at most 131,056. a and b 16-byte aligned. The workspace
+ * carries the error word (14: a wait ran out). Errors: SS24_ERR_DTYPE,
+ * SS24_ERR_SHAPE, SS24_ERR_NULL, SS24_ERR_ALIGN, SS24_ERR_WORKSPACE,
+ * SS24_ERR_CUDA. */
+ss24_status ss24_gemm_int8(const int8_t *a, const float *a_scale, const int8_t *b, const float *b_scale, int64_t m,
+                           int64_t n, int64_t k, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
+                           ss24_stream stream);
+
+/* A paged cache of keys and values in 8 bits (§1: K and V are operands
+ * computed on the fly; §3 formats), with one scale per page and head. Device
+ * memory of the caller. A page holds `page` tokens; token slot t of head h of
+ * page p is the head_dim codes at ((p * kv_heads + h) * page + t) * head_dim,
+ * and stands for code * scale[p * kv_heads + h]. */
+typedef struct {
+    void *k, *v;                /* codes, 16-byte aligned: int8 (SS24_FMT_INT) or E4M3        */
+    float *k_scales, *v_scales; /* [pages][kv_heads]                                          */
+    int32_t kind;               /* SS24_FMT_INT (8 bits) or SS24_FMT_FP8_E4M3                 */
+    int32_t page;               /* tokens per page: 16, 32, 64 or 128                         */
+    int64_t pages;
+    int32_t kv_heads;           /* 1 .. 1024                                                  */
+    int32_t head_dim;           /* 64 or 128                                                  */
+} ss24_kv_cache;
+
+/* The sequences of a call. Sequence s has lengths[s] tokens in the cache, the
+ * new ones included; position j lies in page page_table[s * table_ld + j /
+ * page], slot j % page. Its new tokens are rows starts[s] .. starts[s + 1] - 1
+ * of the token tensors, the last starts[s + 1] - starts[s] positions. The
+ * arrays are device memory and are read by the kernels, so a captured call
+ * follows their contents; the bounds tokens, max_new and max_len are the
+ * host's. Page numbers behind lengths[s] are not read. A sequence that breaks
+ * a bound is left out and a page number outside the cache counts as no keys
+ * (attention) or drops its tokens (append); both are recorded in the
+ * workspace's error word (17: bounds, 16: page number). */
+typedef struct {
+    const int32_t *page_table; /* [seqs][table_ld]                              */
+    const int32_t *starts;     /* [seqs + 1], ascending, within 0 .. tokens     */
+    const int32_t *lengths;    /* [seqs], each 0 .. max_len                     */
+    int64_t seqs, table_ld;    /* table_ld * page >= max_len                    */
+    int64_t tokens;            /* rows of the token tensors                     */
+    int64_t max_new;           /* most new tokens of a sequence, <= tokens      */
+    int64_t max_len;           /* longest lengths[s]                            */
+} ss24_kv_batch;
+
+/* Per-token, per-head rows of head_dim elements: row (t, h) at x + t *
+ * token_stride + h * head_stride elements, 16-byte aligned. */
+typedef struct {
+    void *x;
+    int32_t dtype; /* ss24_dtype */
+    int32_t heads;
+    int64_t token_stride, head_stride;
+} ss24_head_rows;
+
+/* Writes the new tokens' K and V (bf16 or fp32, both the same) into the cache.
+ * Per page and head, over the page's new tokens x of this call:
+ *   s_x = RN(amax |x| / qmax), qmax 127 (INT) or 448 (E4M3)
+ *   scale = s_x, or max(scale before, s_x) where the page holds older tokens of
+ *   the sequence (slots before the first new one)
+ *   code = clamp(rint(RN(x / scale)), -127, 127), or E4M3satfinite(RN(x / scale))
+ * and where the scale of a page with older tokens grew, their codes are formed
+ * again the same way from RN(code * scale before). A zero scale gives zero
+ * codes. The same call made again leaves the cache as it is. New tokens at a
+ * negative position (more new tokens than lengths[s]) are dropped; slots behind
+ * lengths[s], other pages and their scales are left as they were. Pages that
+ * receive tokens belong to one sequence each. max_new and max_len 0: nothing
+ * is launched. Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT,
+ * SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */
+ss24_status ss24_kv_append(const ss24_kv_cache *cache, const ss24_kv_batch *batch, const ss24_head_rows *k,
+                           const ss24_head_rows *v, void *ws, size_t ws_bytes, ss24_stream stream);
+
+/* Bytes of scratch that ss24_kv_attention needs for these sizes (the parts of
+ * the key axis it joins; 0 where it needs none), -1 for invalid arguments. A
+ * function of the sizes and host bounds alone. */
+int64_t ss24_kv_attention_scratch_bytes(const ss24_kv_cache *cache, const ss24_kv_batch *batch, int32_t q_heads);
+
+/* Attention of the new tokens over the cache (their own keys and values
+ * appended before). q: bf16, q_heads a multiple of kv_heads; query head h reads
+ * KV head h / (q_heads / kv_heads). For row (t, h) of the new token at position
+ * i of its sequence, over the keys j < lengths[s], and j <= i with causal = 1:
+ *   z_j = scale q . k_j;  out = sum_j e^{z_j} v_j / sum_j e^{z_j};
+ *   lse = log(sum_j e^{z_j})
+ * with k_j, v_j the values the codes stand for. A row that sees no key gets
+ * out 0 and lse -infinity. out: bf16, q_heads; lse: fp32 [tokens][q_heads] or
+ * NULL. Rows of q outside starts[0] .. starts[seqs] - 1 are left as they were
+ * in out and lse. scratch: device, ss24_kv_attention_scratch_bytes() bytes,
+ * 16-byte aligned, any contents, this call's own until it has run. q is taken
+ * with 11 significant bits below its row's largest magnitude (bf16 has 8), the
+ * products are summed in binary32, the weights e^{z_j - m} s_v enter the second
+ * product in fp16, the sum of weights does not round them. Cache codes of the
+ * tokens seen must be finite; others are not used. Error word: 15 (a wait ran
+ * out), 16, 17. Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT,
+ * SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_ARG (scale not finite, causal),
+ * SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */
+ss24_status ss24_kv_attention(const ss24_head_rows *q, const ss24_kv_cache *cache, const ss24_kv_batch *batch,
+                              float scale, int32_t causal, const ss24_head_rows *out, float *lse, void *scratch,
+                              int64_t scratch_bytes, void *ws, size_t ws_bytes, ss24_stream stream);
+
 /* ---- consumer layouts ------------------------------------------------------ */
 
 /* Bytes of the block-scale tiles of a rows x cols scale matrix (one operand):

@@ -1,0 +1,187 @@
+// New tokens' K and V into the 8-bit paged cache: one scale per (page, head).
+//
+//   s_tok = RN(amax over the page's new tokens / qmax)     qmax 127 (INT8), 448 (E4M3)
+//   s     = max(s_old, s_tok)  where the page holds older tokens, else s_tok
+//   code  = the library's code of RN(x / s); older codes, where s grew, the
+//           code of RN(RN(code_old s_old) / s)
+//
+// The older tokens' values are known only as their codes, so a page whose
+// scale grows rounds them once more; a page written in one call is rounded
+// once. One CTA serves one (page, head) of K or of V: its new tokens are read
+// once into registers, reduced to their amax and written as codes. Bound by
+// memory: 2 (bf16) or 4 bytes read and 1 written per element.
+#include "serve.cuh"
+
+namespace ss24 {
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+template <bool F32> __device__ __forceinline__ void load8(const void *base, int64_t at, float (&v)[8])
+{
+    if constexpr (F32) {
+        const float4 *x = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
+        const float4 a = __ldg(x), b = __ldg(x + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + at));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+}
+
+__device__ __forceinline__ float quotient(float v, const Recip &r)
+{
+    if (r.fast)
+        return div_fast(v, r);
+    return r.b > 0.0f ? __fdiv_rn(v, r.b) : 0.0f;
+}
+
+template <bool FP8> __device__ __forceinline__ uint2 encode8(const float (&v)[8], const Recip &r)
+{
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float q0 = quotient(v[2 * i], r), q1 = quotient(v[2 * i + 1], r);
+        if constexpr (FP8) {
+            w[i >> 1] |= static_cast<uint32_t>(cvt_e4m3x2h(q0, q1)) << (16 * (i & 1));
+        } else {
+            const uint32_t c0 = __float2int_rn(fminf(fmaxf(q0, -127.0f), 127.0f)) & 0xff;
+            const uint32_t c1 = __float2int_rn(fminf(fmaxf(q1, -127.0f), 127.0f)) & 0xff;
+            w[i >> 1] |= (c0 | c1 << 8) << (16 * (i & 1));
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+template <bool FP8> __device__ __forceinline__ void decode8(uint2 c, float s, float (&v)[8])
+{
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = (w[i >> 2] >> (8 * (i & 3))) & 0xff;
+        const float x = FP8 ? e4m3_to_f32(b) : static_cast<float>(static_cast<int8_t>(b));
+        v[i] = __fmul_rn(x, s);
+    }
+}
+
+// CPT: chunks of 8 elements a thread holds, a page's chunks over the block.
+template <bool FP8, bool F32, int CPT>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendParams p)
+{
+    __shared__ float warp_max[kAppendThreads / 32];
+    const KvCache &c = p.cache;
+    int64_t b = blockIdx.x;
+    const int h = static_cast<int>(b % c.kv_heads);
+    b /= c.kv_heads;
+    const int kv = static_cast<int>(b & 1);
+    b >>= 1;
+    const int64_t slot = b % p.page_slots, s = b / p.page_slots;
+    grid_dependency_wait();
+
+    int32_t first, count, len;
+    if (!kv_sequence(p.batch, s, p.err, &first, &count, &len) || count == 0)
+        return;
+    const int32_t begin = len - count; // negative: the first tokens have no place
+    const int64_t pi = ((begin > 0 ? begin : 0) >> c.log2_page) + slot;
+    const int64_t p0 = pi << c.log2_page;
+    const int64_t lo = begin > p0 ? begin : p0, hi = len < p0 + c.page ? len : p0 + c.page;
+    if (lo >= hi)
+        return;
+    const int32_t id = p.batch.table[s * p.batch.table_ld + pi];
+    if (id < 0 || id >= c.pages) {
+        if (threadIdx.x == 0)
+            atomicCAS(p.err, 0, kErrPage);
+        return;
+    }
+    const int fill = static_cast<int>(lo - p0), end = static_cast<int>(hi - p0); // new slots [fill, end)
+    const int64_t page_head = static_cast<int64_t>(id) * c.kv_heads + h;
+    uint8_t *codes = c.codes[kv] + (page_head << c.log2_page) * c.d;
+    const HeadRows &x = p.x[kv];
+    const int64_t row0 = first + (p0 - begin); // the token at slot 0
+    const int cpr = c.d >> 3;                  // chunks per token
+
+    float v[CPT][8];
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        const int ch = threadIdx.x + i * kAppendThreads;
+        const int t = ch / cpr;
+        if (t >= fill && t < end)
+            load8<F32>(x.x, (row0 + t) * x.token_ld + h * x.head_ld + 8 * (ch % cpr), v[i]);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < CPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            amax = fmaxf(amax, fabsf(v[i][j]));
+    for (int o = 16; o; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+    if ((threadIdx.x & 31) == 0)
+        warp_max[threadIdx.x >> 5] = amax;
+    const float had = fill > 0 ? c.scales[kv][page_head] : 0.0f;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w)
+        amax = fmaxf(amax, warp_max[w]);
+    const float s_new = fmaxf(had, __fdiv_rn(amax, FP8 ? 448.0f : 127.0f));
+    const Recip r = make_recip(s_new);
+    if (threadIdx.x == 0)
+        c.scales[kv][page_head] = s_new;
+    const bool grew = fill > 0 && s_new > had;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        const int ch = threadIdx.x + i * kAppendThreads;
+        const int t = ch / cpr;
+        uint2 *at = reinterpret_cast<uint2 *>(codes) + ch;
+        if (t >= fill && t < end) {
+            *at = encode8<FP8>(v[i], r);
+        } else if (grew && t < fill) {
+            decode8<FP8>(*at, had, v[i]);
+            *at = encode8<FP8>(v[i], r);
+        }
+    }
+}
+
+template <bool FP8, bool F32> const void *append_kernel(int cpt)
+{
+    if (cpt <= 1)
+        return reinterpret_cast<const void *>(kv_append_kernel<FP8, F32, 1>);
+    if (cpt <= 2)
+        return reinterpret_cast<const void *>(kv_append_kernel<FP8, F32, 2>);
+    if (cpt <= 4)
+        return reinterpret_cast<const void *>(kv_append_kernel<FP8, F32, 4>);
+    return reinterpret_cast<const void *>(kv_append_kernel<FP8, F32, 8>);
+}
+
+} // namespace
+
+cudaError_t launch_kv_append(const KvAppendParams &p, int x_f32, cudaStream_t stream)
+{
+    const int cpt = (p.cache.page * p.cache.d / 8 + kAppendThreads - 1) / kAppendThreads;
+    const void *k = p.cache.fp8 ? (x_f32 ? append_kernel<true, true>(cpt) : append_kernel<true, false>(cpt))
+                                : (x_f32 ? append_kernel<false, true>(cpt) : append_kernel<false, false>(cpt));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch.seqs * p.page_slots * 2 * p.cache.kv_heads));
+    cfg.blockDim = dim3(kAppendThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    KvAppendParams pp = p;
+    void *args[1] = {&pp};
+    return cudaLaunchKernelExC(&cfg, k, args);
+}
+
+} // namespace ss24

@@ -51,6 +51,23 @@ class Outputs(ctypes.Structure):
                 ("tensor_scale", ctypes.c_void_p), ("meta", ctypes.c_void_p)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("kind", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("table_ld", ctypes.c_int64), ("tokens", ctypes.c_int64),
+                ("max_new", ctypes.c_int64), ("max_len", ctypes.c_int64)]
+
+
+class HeadRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 class SS24Error(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -62,6 +79,9 @@ _P = ctypes.c_void_p
 _S = ctypes.c_size_t
 _OP = ctypes.POINTER(Operand)
 _OUT = ctypes.POINTER(Outputs)
+_KVC = ctypes.POINTER(KvCache)
+_KVB = ctypes.POINTER(KvBatch)
+_HR = ctypes.POINTER(HeadRows)
 
 _SIGNATURES = {
     "ss24_workspace_bytes": (ctypes.c_size_t, []),
@@ -97,6 +117,12 @@ _SIGNATURES = {
                                               _P, _P]),
     "ss24_sparse_gemm_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                             _P, _P, _S, _P]),
+    "ss24_gemm_int8": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P,
+                                      ctypes.c_int32, ctypes.c_int64, _P, _S, _P]),
+    "ss24_kv_append": (ctypes.c_int, [_KVC, _KVB, _HR, _HR, _P, _S, _P]),
+    "ss24_kv_attention_scratch_bytes": (ctypes.c_int64, [_KVC, _KVB, ctypes.c_int32]),
+    "ss24_kv_attention": (ctypes.c_int, [_HR, _KVC, _KVB, ctypes.c_float, ctypes.c_int32, _HR, _P, _P,
+                                         ctypes.c_int64, _P, _S, _P]),
     "ss24_encode_e4m3": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P]),
     "ss24_decode_e4m3": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P]),
     "ss24_encode_e2m1": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P]),
@@ -445,6 +471,168 @@ def sparse_gemm_fp8(a, b, y=None, ws=None, stream=None):
                                       _ptr(b["values"]), _ptr(b["tensor_scale"]), m, n, k, _ptr(y), ws.ptr,
                                       ws.nbytes, _stream(stream)), "ss24_sparse_gemm_fp8")
     return y
+
+
+# ---- serving in 8 bits -------------------------------------------------------
+
+def _on(device, **tensors):
+    """Every given tensor lies on `device`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _int8_rows(d, name):
+    """Codes and scales of an INT8 operand with one scale per row."""
+    v, s = d["values"], d["scales"]
+    if v.dtype != torch.int8 or v.dim() != 2 or not v.is_contiguous():
+        raise ValueError(f"{name}['values'] must be contiguous int8 [rows, k]")
+    if s.dtype != torch.float32 or s.numel() != v.shape[0] or not s.is_contiguous():
+        raise ValueError(f"{name}['scales'] must be contiguous float32, one per row")
+    return v, s
+
+
+def gemm_int8(a, b, dtype=torch.bfloat16, y=None, ws=None, stream=None):
+    """Y = diag(s_a) A B^T diag(s_b) on the INT8 tensor cores (ss24_gemm_int8).
+    a, b: the dicts of dense INT8 passes with one scale per row over [m, k]
+    tokens and [n, k] channels (``values`` int8, ``scales`` float32 [rows, 1]).
+    Returns [m, n] in `dtype` (bfloat16 or float32), or fills `y` (its dtype;
+    the columns contiguous, any row stride)."""
+    av, sa = _int8_rows(a, "a")
+    bv, sb = _int8_rows(b, "b")
+    m, k = av.shape
+    n = bv.shape[0]
+    if bv.shape[1] != k:
+        raise ValueError("a and b differ in k")
+    dev = av.device
+    if y is None:
+        y = torch.empty((m, n), dtype=dtype, device=dev)
+    if y.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("y must be bfloat16 or float32")
+    if tuple(y.shape) != (m, n) or (n > 1 and y.stride(1) != 1) or (m > 1 and y.stride(0) < n):
+        raise ValueError("y must be [m, n] with contiguous columns and rows that do not overlap")
+    _on(dev, a_scales=sa, b=bv, b_scales=sb, y=y)
+    with torch.cuda.device(dev):
+        ws = ws or default_workspace(dev)
+        _check(lib().ss24_gemm_int8(_ptr(av), _ptr(sa), _ptr(bv), _ptr(sb), m, n, k, _ptr(y),
+                                    F32 if y.dtype == torch.float32 else BF16, max(y.stride(0), n), ws.ptr, ws.nbytes,
+                                    _stream(stream)), "ss24_gemm_int8")
+    return y
+
+
+def kv_cache(pages, kv_heads, head_dim, page=64, fmt="int", device=None):
+    """An empty 8-bit paged cache (ss24_kv_cache) as a dict: codes ``k``, ``v``
+    [pages, kv_heads, page, head_dim] (int8 for "int", uint8 E4M3 for "fp8"),
+    ``k_scales``, ``v_scales`` float32 [pages, kv_heads], ``page`` and ``fmt``."""
+    if fmt not in ("int", "fp8"):
+        raise ValueError("the cache's format is 'int' (8 bits) or 'fp8'")
+    dt = torch.int8 if fmt == "int" else torch.uint8
+    dev = torch.device(device or "cuda")
+    c = {n: torch.zeros((pages, kv_heads, page, head_dim), dtype=dt, device=dev) for n in ("k", "v")}
+    c.update({n: torch.zeros((pages, kv_heads), dtype=torch.float32, device=dev) for n in ("k_scales", "v_scales")})
+    return {**c, "page": page, "fmt": fmt}
+
+
+def _kv_cache(cache) -> KvCache:
+    k, v, ks, vs, fmt = (cache[n] for n in ("k", "v", "k_scales", "v_scales", "fmt"))
+    if fmt not in ("int", "fp8"):
+        raise ValueError("the cache's format is 'int' (8 bits) or 'fp8'")
+    dt = torch.int8 if fmt == "int" else torch.uint8
+    for t in (k, v):
+        if t.dtype != dt or t.dim() != 4 or not t.is_contiguous() or t.shape != k.shape:
+            raise ValueError(f"the cache's codes must be contiguous {dt} [pages, kv_heads, page, head_dim]")
+    for t in (ks, vs):
+        if t.dtype != torch.float32 or t.shape != k.shape[:2] or not t.is_contiguous():
+            raise ValueError("the cache's scales must be contiguous float32 [pages, kv_heads]")
+    if k.shape[2] != cache["page"]:
+        raise ValueError("the cache's page is not its codes' third dimension")
+    _on(k.device, v=v, k_scales=ks, v_scales=vs)
+    return KvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), _FMT[fmt], k.shape[2], k.shape[0],
+                   k.shape[1], k.shape[3])
+
+
+def _kv_batch(cache, tokens, page_table, starts, lengths, max_new, max_len) -> KvBatch:
+    seqs = lengths.numel()
+    for name, t, shape in (("page_table", page_table, (seqs, page_table.shape[-1])), ("starts", starts, (seqs + 1,)),
+                           ("lengths", lengths, (seqs,))):
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or (name != "page_table" and not t.is_contiguous()):
+            raise ValueError(f"{name} must be int32 {list(shape)}")
+    ld = page_table.stride(0) if seqs > 1 else page_table.shape[1]
+    if (page_table.shape[1] > 1 and page_table.stride(1) != 1) or ld < page_table.shape[1]:
+        raise ValueError("page_table must have contiguous rows")
+    _on(cache["k"].device, page_table=page_table, starts=starts, lengths=lengths)
+    room = page_table.shape[1] * cache["page"]
+    max_len = room if max_len is None else int(max_len)
+    if max_len > room:
+        raise ValueError("max_len does not fit the page table")
+    max_new = tokens if max_new is None else min(int(max_new), tokens)
+    return KvBatch(page_table.data_ptr(), starts.data_ptr(), lengths.data_ptr(), seqs, ld, tokens, max_new, max_len)
+
+
+def _head_rows(x, name, head_dim) -> HeadRows:
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    if x.dim() != 3 or x.shape[2] != head_dim or x.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens, heads, {head_dim}] with contiguous rows")
+    # a stride that only one row would use is free
+    ts = x.stride(0) if x.shape[0] > 1 else x.shape[1] * head_dim
+    hs = x.stride(1) if x.shape[1] > 1 else head_dim
+    return HeadRows(x.data_ptr(), BF16 if x.dtype == torch.bfloat16 else F32, x.shape[1], ts, hs)
+
+
+def kv_append(cache, k, v, page_table, starts, lengths, max_new=None, max_len=None, ws=None, stream=None):
+    """New tokens' k, v [tokens, kv_heads, head_dim] (bfloat16 or float32, any
+    token and head strides) into the cache (ss24_kv_append), in place; returns
+    it. page_table int32 [seqs, most pages], starts int32 [seqs + 1], lengths
+    int32 [seqs] (the new tokens included). max_new, max_len: bounds that the
+    host knows; by default the loosest ones."""
+    c = _kv_cache(cache)
+    if k.shape != v.shape:
+        raise ValueError("k and v differ in shape")
+    kr, vr = _head_rows(k, "k", c.head_dim), _head_rows(v, "v", c.head_dim)
+    b = _kv_batch(cache, k.shape[0], page_table, starts, lengths, max_new, max_len)
+    dev = cache["k"].device
+    _on(dev, k=k, v=v)
+    with torch.cuda.device(dev):
+        ws = ws or default_workspace(dev)
+        _check(lib().ss24_kv_append(ctypes.byref(c), ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr), ws.ptr,
+                                    ws.nbytes, _stream(stream)), "ss24_kv_append")
+    return cache
+
+
+def kv_attention(q, cache, page_table, starts, lengths, scale=None, causal=True, max_new=None, max_len=None, out=None,
+                 lse=False, ws=None, stream=None):
+    """Attention of the new tokens' q [tokens, q_heads, head_dim] (bfloat16)
+    over the cache (ss24_kv_attention); the sequences as in kv_append. scale:
+    1 / sqrt(head_dim) by default. Returns out [tokens, q_heads, head_dim]
+    (bfloat16), or (out, lse) with lse=True or an lse tensor (float32 [tokens,
+    q_heads]). Tight max_new and max_len choose a better split of the work."""
+    c = _kv_cache(cache)
+    qr = _head_rows(q, "q", c.head_dim)
+    b = _kv_batch(cache, q.shape[0], page_table, starts, lengths, max_new, max_len)
+    dev = cache["k"].device
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    with torch.cuda.device(dev), torch.cuda.stream(s):
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        if lse is True:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        elif lse is False:
+            lse = None
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+            raise ValueError("lse must be contiguous float32 [tokens, q_heads]")
+        outr = _head_rows(out, "out", c.head_dim)
+        _on(dev, q=q, out=out, lse=lse)
+        ws = ws or default_workspace(dev)
+        n = lib().ss24_kv_attention_scratch_bytes(ctypes.byref(c), ctypes.byref(b), q.shape[1])
+        scratch = torch.empty(n, dtype=torch.uint8, device=dev) if n > 0 else None
+        _check(lib().ss24_kv_attention(ctypes.byref(qr), ctypes.byref(c), ctypes.byref(b),
+                                       c.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)),
+                                       ctypes.byref(outr), _ptr(lse), _ptr(scratch), max(n, 0), ws.ptr, ws.nbytes,
+                                       _stream(s)), "ss24_kv_attention")
+    return out if lse is None else (out, lse)
 
 
 def bits_per_element(fmt="none", bits=8, group=0, pattern=SPARSE_24, k=4096, with_scales=False) -> float:
