@@ -475,11 +475,34 @@ def sparse_gemm_fp8(a, b, y=None, ws=None, stream=None):
 
 # ---- serving in 8 bits -------------------------------------------------------
 
-def _on(device, **tensors):
-    """Every given tensor lies on `device`."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+# These wrappers sit on the path of a decode step, where a kernel takes a few
+# microseconds: they check with few attribute reads, enter no context that is
+# already current and ask for the stream's raw handle only.
+
+def _same_device(index, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on different devices: {t.device} and index {index}")
+
+
+def _enqueue(index, stream, name, *args):
+    """The C call `name`(*args, stream) with device `index` current, on `stream`
+    or that device's current stream."""
+    if index < 0:
+        raise ValueError(f"{name} needs CUDA tensors")
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, raw)
+    if st != OK:
+        raise SS24Error(st, name)
+
+
+def _workspace(ws, t):
+    return ws if ws is not None else default_workspace(t.device)
 
 
 def _int8_rows(d, name):
@@ -500,68 +523,76 @@ def gemm_int8(a, b, dtype=torch.bfloat16, y=None, ws=None, stream=None):
     the columns contiguous, any row stride)."""
     av, sa = _int8_rows(a, "a")
     bv, sb = _int8_rows(b, "b")
-    m, k = av.shape
-    n = bv.shape[0]
-    if bv.shape[1] != k:
+    (m, k), (n, kb) = av.shape, bv.shape
+    if kb != k:
         raise ValueError("a and b differ in k")
-    dev = av.device
     if y is None:
-        y = torch.empty((m, n), dtype=dtype, device=dev)
-    if y.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("y must be bfloat16 or float32")
-    if tuple(y.shape) != (m, n) or (n > 1 and y.stride(1) != 1) or (m > 1 and y.stride(0) < n):
-        raise ValueError("y must be [m, n] with contiguous columns and rows that do not overlap")
-    _on(dev, a_scales=sa, b=bv, b_scales=sb, y=y)
-    with torch.cuda.device(dev):
-        ws = ws or default_workspace(dev)
-        _check(lib().ss24_gemm_int8(_ptr(av), _ptr(sa), _ptr(bv), _ptr(sb), m, n, k, _ptr(y),
-                                    F32 if y.dtype == torch.float32 else BF16, max(y.stride(0), n), ws.ptr, ws.nbytes,
-                                    _stream(stream)), "ss24_gemm_int8")
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise TypeError("y must be bfloat16 or float32")
+        y, ld = av.new_empty((m, n), dtype=dtype), n
+    else:
+        if y.dtype is not torch.bfloat16 and y.dtype is not torch.float32:
+            raise TypeError("y must be bfloat16 or float32")
+        if tuple(y.shape) != (m, n) or (n > 1 and y.stride(1) != 1) or (m > 1 and y.stride(0) < n):
+            raise ValueError("y must be [m, n] with contiguous columns and rows that do not overlap")
+        ld = max(y.stride(0), n)
+    index = av.get_device()
+    _same_device(index, sa, bv, sb, y)
+    ws = _workspace(ws, av)
+    _enqueue(index, stream, "ss24_gemm_int8", av.data_ptr(), sa.data_ptr(), bv.data_ptr(), sb.data_ptr(), m, n, k,
+             y.data_ptr(), F32 if y.dtype is torch.float32 else BF16, ld, ws.ptr, ws.nbytes)
     return y
+
+
+_KV_DTYPE = {"int": (torch.int8, FMT_INT), "fp8": (torch.uint8, FMT_FP8)}
 
 
 def kv_cache(pages, kv_heads, head_dim, page=64, fmt="int", device=None):
     """An empty 8-bit paged cache (ss24_kv_cache) as a dict: codes ``k``, ``v``
     [pages, kv_heads, page, head_dim] (int8 for "int", uint8 E4M3 for "fp8"),
     ``k_scales``, ``v_scales`` float32 [pages, kv_heads], ``page`` and ``fmt``."""
-    if fmt not in ("int", "fp8"):
+    if fmt not in _KV_DTYPE:
         raise ValueError("the cache's format is 'int' (8 bits) or 'fp8'")
-    dt = torch.int8 if fmt == "int" else torch.uint8
     dev = torch.device(device or "cuda")
-    c = {n: torch.zeros((pages, kv_heads, page, head_dim), dtype=dt, device=dev) for n in ("k", "v")}
+    c = {n: torch.zeros((pages, kv_heads, page, head_dim), dtype=_KV_DTYPE[fmt][0], device=dev) for n in ("k", "v")}
     c.update({n: torch.zeros((pages, kv_heads), dtype=torch.float32, device=dev) for n in ("k_scales", "v_scales")})
     return {**c, "page": page, "fmt": fmt}
 
 
 def _kv_cache(cache) -> KvCache:
-    k, v, ks, vs, fmt = (cache[n] for n in ("k", "v", "k_scales", "v_scales", "fmt"))
-    if fmt not in ("int", "fp8"):
+    k, v, ks, vs, fmt = cache["k"], cache["v"], cache["k_scales"], cache["v_scales"], cache["fmt"]
+    if fmt not in _KV_DTYPE:
         raise ValueError("the cache's format is 'int' (8 bits) or 'fp8'")
-    dt = torch.int8 if fmt == "int" else torch.uint8
-    for t in (k, v):
-        if t.dtype != dt or t.dim() != 4 or not t.is_contiguous() or t.shape != k.shape:
-            raise ValueError(f"the cache's codes must be contiguous {dt} [pages, kv_heads, page, head_dim]")
-    for t in (ks, vs):
-        if t.dtype != torch.float32 or t.shape != k.shape[:2] or not t.is_contiguous():
-            raise ValueError("the cache's scales must be contiguous float32 [pages, kv_heads]")
-    if k.shape[2] != cache["page"]:
+    dt, kind = _KV_DTYPE[fmt]
+    shape = k.shape
+    if (k.dtype is not dt or v.dtype is not dt or len(shape) != 4 or v.shape != shape or not k.is_contiguous()
+            or not v.is_contiguous()):
+        raise ValueError(f"the cache's codes must be contiguous {dt} [pages, kv_heads, page, head_dim]")
+    pages, heads, page, d = shape
+    if (ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or ks.shape != (pages, heads)
+            or vs.shape != (pages, heads) or not ks.is_contiguous() or not vs.is_contiguous()):
+        raise ValueError("the cache's scales must be contiguous float32 [pages, kv_heads]")
+    if page != cache["page"]:
         raise ValueError("the cache's page is not its codes' third dimension")
-    _on(k.device, v=v, k_scales=ks, v_scales=vs)
-    return KvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), _FMT[fmt], k.shape[2], k.shape[0],
-                   k.shape[1], k.shape[3])
+    _same_device(k.get_device(), v, ks, vs)
+    return KvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kind, page, pages, heads, d)
 
 
 def _kv_batch(cache, tokens, page_table, starts, lengths, max_new, max_len) -> KvBatch:
     seqs = lengths.numel()
-    for name, t, shape in (("page_table", page_table, (seqs, page_table.shape[-1])), ("starts", starts, (seqs + 1,)),
-                           ("lengths", lengths, (seqs,))):
-        if t.dtype != torch.int32 or tuple(t.shape) != shape or (name != "page_table" and not t.is_contiguous()):
-            raise ValueError(f"{name} must be int32 {list(shape)}")
-    ld = page_table.stride(0) if seqs > 1 else page_table.shape[1]
-    if (page_table.shape[1] > 1 and page_table.stride(1) != 1) or ld < page_table.shape[1]:
+    if (lengths.dtype is not torch.int32 or lengths.dim() != 1 or not lengths.is_contiguous()):
+        raise ValueError("lengths must be int32 [seqs]")
+    if starts.dtype is not torch.int32 or starts.shape != (seqs + 1,) or not starts.is_contiguous():
+        raise ValueError(f"starts must be int32 [{seqs + 1}]")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != seqs:
+        raise ValueError(f"page_table must be int32 [{seqs}, most pages]")
+    width = page_table.shape[1]
+    row, col = page_table.stride()
+    ld = row if seqs > 1 else width
+    if (width > 1 and col != 1) or ld < width:
         raise ValueError("page_table must have contiguous rows")
-    _on(cache["k"].device, page_table=page_table, starts=starts, lengths=lengths)
-    room = page_table.shape[1] * cache["page"]
+    _same_device(cache["k"].get_device(), page_table, starts, lengths)
+    room = width * cache["page"]
     max_len = room if max_len is None else int(max_len)
     if max_len > room:
         raise ValueError("max_len does not fit the page table")
@@ -570,14 +601,15 @@ def _kv_batch(cache, tokens, page_table, starts, lengths, max_new, max_len) -> K
 
 
 def _head_rows(x, name, head_dim) -> HeadRows:
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
         raise TypeError(f"{name} must be bfloat16 or float32")
     if x.dim() != 3 or x.shape[2] != head_dim or x.stride(2) != 1:
         raise ValueError(f"{name} must be [tokens, heads, {head_dim}] with contiguous rows")
     # a stride that only one row would use is free
-    ts = x.stride(0) if x.shape[0] > 1 else x.shape[1] * head_dim
-    hs = x.stride(1) if x.shape[1] > 1 else head_dim
-    return HeadRows(x.data_ptr(), BF16 if x.dtype == torch.bfloat16 else F32, x.shape[1], ts, hs)
+    tokens, heads, _ = x.shape
+    ts, hs, _ = x.stride()
+    return HeadRows(x.data_ptr(), BF16 if x.dtype is torch.bfloat16 else F32, heads,
+                    ts if tokens > 1 else heads * head_dim, hs if heads > 1 else head_dim)
 
 
 def kv_append(cache, k, v, page_table, starts, lengths, max_new=None, max_len=None, ws=None, stream=None):
@@ -591,12 +623,10 @@ def kv_append(cache, k, v, page_table, starts, lengths, max_new=None, max_len=No
         raise ValueError("k and v differ in shape")
     kr, vr = _head_rows(k, "k", c.head_dim), _head_rows(v, "v", c.head_dim)
     b = _kv_batch(cache, k.shape[0], page_table, starts, lengths, max_new, max_len)
-    dev = cache["k"].device
-    _on(dev, k=k, v=v)
-    with torch.cuda.device(dev):
-        ws = ws or default_workspace(dev)
-        _check(lib().ss24_kv_append(ctypes.byref(c), ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr), ws.ptr,
-                                    ws.nbytes, _stream(stream)), "ss24_kv_append")
+    index = cache["k"].get_device()
+    _same_device(index, k, v)
+    ws = _workspace(ws, k)
+    _enqueue(index, stream, "ss24_kv_append", c, b, kr, vr, ws.ptr, ws.nbytes)
     return cache
 
 
@@ -607,31 +637,32 @@ def kv_attention(q, cache, page_table, starts, lengths, scale=None, causal=True,
     1 / sqrt(head_dim) by default. Returns out [tokens, q_heads, head_dim]
     (bfloat16), or (out, lse) with lse=True or an lse tensor (float32 [tokens,
     q_heads]). Tight max_new and max_len choose a better split of the work."""
+    if stream is not None and stream != torch.cuda.current_stream(stream.device):
+        # what is allocated here belongs to the stream that uses it
+        with torch.cuda.stream(stream):
+            return kv_attention(q, cache, page_table, starts, lengths, scale, causal, max_new, max_len, out, lse, ws)
     c = _kv_cache(cache)
-    qr = _head_rows(q, "q", c.head_dim)
+    d = c.head_dim
+    qr = _head_rows(q, "q", d)
     b = _kv_batch(cache, q.shape[0], page_table, starts, lengths, max_new, max_len)
-    dev = cache["k"].device
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    with torch.cuda.device(dev), torch.cuda.stream(s):
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        if lse is True:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-        elif lse is False:
-            lse = None
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
-            raise ValueError("lse must be contiguous float32 [tokens, q_heads]")
-        outr = _head_rows(out, "out", c.head_dim)
-        _on(dev, q=q, out=out, lse=lse)
-        ws = ws or default_workspace(dev)
-        n = lib().ss24_kv_attention_scratch_bytes(ctypes.byref(c), ctypes.byref(b), q.shape[1])
-        scratch = torch.empty(n, dtype=torch.uint8, device=dev) if n > 0 else None
-        _check(lib().ss24_kv_attention(ctypes.byref(qr), ctypes.byref(c), ctypes.byref(b),
-                                       c.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)),
-                                       ctypes.byref(outr), _ptr(lse), _ptr(scratch), max(n, 0), ws.ptr, ws.nbytes,
-                                       _stream(s)), "ss24_kv_attention")
+    if out is None:
+        out = q.new_empty(q.shape)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is True:
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+    elif lse is False:
+        lse = None
+    elif lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [tokens, q_heads]")
+    outr = _head_rows(out, "out", d)
+    index = cache["k"].get_device()
+    _same_device(index, q, out, lse)
+    ws = _workspace(ws, q)
+    n = lib().ss24_kv_attention_scratch_bytes(c, b, qr.heads)
+    scratch = q.new_empty((n,), dtype=torch.uint8) if n > 0 else None
+    _enqueue(index, None, "ss24_kv_attention", qr, c, b, d ** -0.5 if scale is None else float(scale),
+             1 if causal else 0, outr, _ptr(lse), _ptr(scratch), max(n, 0), ws.ptr, ws.nbytes)
     return out if lse is None else (out, lse)
 
 
