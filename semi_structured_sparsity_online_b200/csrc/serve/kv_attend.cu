@@ -19,31 +19,11 @@
 // (rounded once, 2^-11 relative) and its small values are small next to the
 // sum they enter. M moves only when a value exceeds it by 2^8. The denominator
 // sums w / s_v in binary32. Scales s_v below 2^-100 count as 2^-100.
-#include "serve.cuh"
+#include "kv_attend.cuh"
 
 namespace ss24 {
 
 namespace {
-
-constexpr float kLn2 = 0.693147180559945f;
-
-// four 8-bit codes -> two fp16 pairs, exact
-template <bool FP8> __device__ __forceinline__ void codes4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    if constexpr (FP8) {
-        lo = e4m3x2h_to_f16x2(static_cast<uint16_t>(w));
-        hi = e4m3x2h_to_f16x2(static_cast<uint16_t>(w >> 16));
-    } else {
-        // 0x6400 | u is 1024 + u; u = code + 128
-        const uint32_t u = w ^ 0x80808080u;
-        const __half2 off = __half2half2(__ushort_as_half(0x6480)); // 1152
-        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
-        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
-        lo = *reinterpret_cast<const uint32_t *>(&x);
-        hi = *reinterpret_cast<const uint32_t *>(&y);
-    }
-}
 
 // bytes i of a and of b (i = 0..3) -> four fp16 pairs (a_i, b_i)
 template <bool FP8> __device__ __forceinline__ void pairs4_to_f16(uint32_t a, uint32_t b, uint32_t (&out)[4])
@@ -66,19 +46,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 __device__ __forceinline__ uint4 load_codes16(const uint8_t *p)
@@ -129,24 +96,6 @@ __device__ __forceinline__ void load_keys(Keys16<D> &t, const KvAttendParams &p,
     }
     t.ks = __ldg(p.cache.scales[0] + ph);
     t.vs = __ldg(p.cache.scales[1] + ph);
-}
-
-// Row r of a (sequence, KV head): its token row, its query head, and the keys
-// it sees.
-struct RowAt {
-    int64_t token;
-    int32_t head, limit;
-};
-__device__ __forceinline__ RowAt row_at(const KvAttendParams &p, int64_t r, int h, int32_t first, int32_t count,
-                                        int32_t len)
-{
-    const int32_t i = static_cast<int32_t>(r / p.group);
-    RowAt a;
-    a.token = first + i;
-    a.head = h * p.group + static_cast<int32_t>(r - static_cast<int64_t>(i) * p.group);
-    const int32_t seen = len - count + i + 1;
-    a.limit = !p.causal ? len : seen < 0 ? 0 : seen;
-    return a;
 }
 
 // NT: n tiles of 8 rows; WARPS warps take turns on the part's 16-key steps.
@@ -447,7 +396,10 @@ cudaError_t launch(const void *k, int64_t grid, int threads, const KvAttendParam
     return cudaLaunchKernelExC(&cfg, k, args);
 }
 
+// Up to 16 rows per (sequence, KV head) go to the kernel above, in tiles of 8
+// or 16; more rows to the tensor-memory kernel in tiles of 256.
 bool narrow(const KvAttendParams &p) { return p.batch.max_new * p.group <= 8; }
+bool wide(const KvAttendParams &p) { return p.batch.max_new * p.group > 16; }
 
 template <int D, bool FP8> const void *rows_kernel(bool one)
 {
@@ -459,26 +411,32 @@ template <int D, bool FP8> const void *rows_kernel(bool one)
 
 void kv_attend_plan(KvAttendParams *p)
 {
-    const bool one = narrow(*p);
     const int64_t rows = p->batch.max_new * p->group;
-    p->row_tiles = static_cast<int32_t>(ceil_div(rows, one ? 8 : 16));
+    const int64_t len = p->batch.max_len > 0 ? p->batch.max_len : 1;
+    const int64_t tile = wide(*p) ? kTileRows : narrow(*p) ? 8 : 16;
+    p->row_tiles = static_cast<int32_t>(ceil_div(rows, tile));
     const int64_t ctas = p->batch.seqs * p->cache.kv_heads * p->row_tiles;
-    const int64_t step = one ? 128 : 64;
-    int64_t splits = ctas > 0 ? 148 * 4 / ctas : 1;
-    const int64_t most = ceil_div(p->batch.max_len, 2 * step);
+    // parts of the key axis: enough CTAs to fill the SMs, each with a few steps
+    const int64_t step = narrow(*p) || wide(*p) ? 128 : 64;
+    int64_t splits = ctas > 0 ? 148 * (wide(*p) ? 1 : 4) / ctas : 1;
+    const int64_t most = ceil_div(len, 2 * step);
     splits = splits > most ? most : splits;
     splits = splits < 1 ? 1 : splits;
-    p->split_keys = static_cast<int32_t>(ceil_div(ceil_div(p->batch.max_len > 0 ? p->batch.max_len : 1, splits), step) * step);
-    p->splits = static_cast<int32_t>(ceil_div(p->batch.max_len > 0 ? p->batch.max_len : 1, p->split_keys));
+    p->split_keys = static_cast<int32_t>(ceil_div(ceil_div(len, splits), step) * step);
+    p->splits = static_cast<int32_t>(ceil_div(len, p->split_keys));
 }
 
 cudaError_t launch_kv_attend(const KvAttendParams &p, cudaStream_t stream)
 {
-    const bool one = narrow(p);
-    const void *k = p.cache.d == 128 ? (p.cache.fp8 ? rows_kernel<128, true>(one) : rows_kernel<128, false>(one))
-                                     : (p.cache.fp8 ? rows_kernel<64, true>(one) : rows_kernel<64, false>(one));
-    const int64_t grid = p.batch.seqs * p.cache.kv_heads * p.row_tiles * p.splits;
-    cudaError_t e = launch(k, grid, one ? 256 : 128, p, stream);
+    cudaError_t e;
+    if (wide(p)) {
+        e = launch_kv_attend_tiles(p, stream);
+    } else {
+        const bool one = narrow(p);
+        const void *k = p.cache.d == 128 ? (p.cache.fp8 ? rows_kernel<128, true>(one) : rows_kernel<128, false>(one))
+                                         : (p.cache.fp8 ? rows_kernel<64, true>(one) : rows_kernel<64, false>(one));
+        e = launch(k, p.batch.seqs * p.cache.kv_heads * p.row_tiles * p.splits, one ? 256 : 128, p, stream);
+    }
     if (e != cudaSuccess || p.splits <= 1)
         return e;
     const void *join = p.cache.d == 128 ? reinterpret_cast<const void *>(kv_attend_join_kernel<128>)

@@ -1,0 +1,64 @@
+// What the attention kernels share: decoding of codes, query rows.
+#pragma once
+
+#include "serve.cuh"
+
+namespace ss24 {
+
+constexpr float kLn2 = 0.693147180559945f;
+
+// four 8-bit codes -> two fp16 pairs, exact
+template <bool FP8> __device__ __forceinline__ void codes4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    if constexpr (FP8) {
+        lo = e4m3x2h_to_f16x2(static_cast<uint16_t>(w));
+        hi = e4m3x2h_to_f16x2(static_cast<uint16_t>(w >> 16));
+    } else {
+        // 0x6400 | u is 1024 + u; u = code + 128
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half(0x6480)); // 1152
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+        lo = *reinterpret_cast<const uint32_t *>(&x);
+        hi = *reinterpret_cast<const uint32_t *>(&y);
+    }
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Row r of a (sequence, KV head): its token row, its query head, and the keys
+// it sees.
+struct RowAt {
+    int64_t token;
+    int32_t head, limit;
+};
+__device__ __forceinline__ RowAt row_at(const KvAttendParams &p, int64_t r, int h, int32_t first, int32_t count,
+                                        int32_t len)
+{
+    const int32_t i = static_cast<int32_t>(r / p.group);
+    RowAt a;
+    a.token = first + i;
+    a.head = h * p.group + static_cast<int32_t>(r - static_cast<int64_t>(i) * p.group);
+    const int32_t seen = len - count + i + 1;
+    a.limit = !p.causal ? len : seen < 0 ? 0 : seen;
+    return a;
+}
+
+// Attention on the 5th-generation tensor cores, tiles of 128 or 256 rows
+// (kv_attend_tiles.cu).
+constexpr int kTileRows = 256;
+cudaError_t launch_kv_attend_tiles(const KvAttendParams &p, cudaStream_t stream);
+
+} // namespace ss24
