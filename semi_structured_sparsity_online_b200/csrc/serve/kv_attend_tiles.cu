@@ -8,10 +8,10 @@
 //             shared memory in fp16, takes its row of S = q K^T from tensor
 //             memory, forms the weights and writes them back as fp16 over S;
 //             row maxima and sums need no shuffle
-//   8-11      codes of K and V from the pages to fp16 in shared memory, a ring
-//             of stages in the 128-byte swizzle that the MMA reads
-//   12        one lane issues the MMAs: S (K-major operands) and O += P V with
+//   8         one lane issues the MMAs: S (K-major operands) and O += P V with
 //             P in tensor memory and V as it lies (MN-major)
+//   9-15      codes of K and V from the pages to fp16 in shared memory, a ring
+//             of stages in the 128-byte swizzle that the MMA reads
 // The two row tiles take turns: while one warpgroup works on its S, the
 // tensor cores serve the other. A new S overwrites the weights of the step
 // before; MMAs of one thread run in order, and the commit behind S(j + 1) also
@@ -24,15 +24,21 @@ namespace ss24 {
 
 namespace {
 
-constexpr int kTileThreads = 416;
+constexpr int kTileThreads = 512;
+// 512 threads start with 128 registers each; 2 x 128 x (176 + 80) is the same sum
+constexpr int kRegsRows = 176, kRegsRest = 80;
 constexpr int kKeys = 128;   // keys per step
-constexpr int kRing = 5;     // stages: K and V of a step take one each
+constexpr int kConvWarps = 7;
+constexpr int kRing = 4;     // fp16 stages: K and V of a step take one each
+constexpr int kRaw = 2;      // stages of codes on their way from the pages
 constexpr int kScaleRing = 4; // steps of page scales
 
 template <int D> struct TileShape {
     static constexpr uint32_t kStage = kKeys * D * 2; // also a row tile of q
     static constexpr uint32_t kAtom = kKeys * 128;    // 128 rows x 128 bytes
-    static constexpr size_t kSmem = 1024 + (2 + kRing) * kStage + kScaleRing * 8 * 16 + 256;
+    static constexpr uint32_t kCodes = kKeys * D;     // a stage's codes
+    static constexpr uint32_t kTiles = (2 + kRing) * kStage + kRaw * kCodes;
+    static constexpr size_t kSmem = 1024 + kTiles + kScaleRing * 8 * 16 + 256;
     static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -42,8 +48,26 @@ __host__ __device__ constexpr uint32_t f16_idesc(int n, bool b_mn)
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+template <int N> __device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;"
+        : "=f"(r)
+        : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
+}
+
 struct Bars {
-    uint64_t kv_full[kRing], kv_empty[kRing], q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t kv_full[kRing], kv_empty[kRing], q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
 };
 
 // 16-byte chunk c (8 fp16) of row r in a tile of D / 64 swizzled atoms.
@@ -65,7 +89,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     uint8_t *gen = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t sq = base, skv = base + 2 * S::kStage;
-    float4 *scales = reinterpret_cast<float4 *>(gen + (2 + kRing) * S::kStage); // [kScaleRing][8]: s_k, log2 s_v, 1 / s_v
+    float4 *scales = reinterpret_cast<float4 *>(gen + S::kTiles); // [kScaleRing][8]: s_k, log2 s_v, 1 / s_v
     Bars *bars = reinterpret_cast<Bars *>(scales + kScaleRing * 8);
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(bars + 1);
 
@@ -95,18 +119,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
 
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(&bars->kv_full[i], 128);
+            mbar_init(&bars->kv_full[i], 32 * kConvWarps);
             mbar_init(&bars->kv_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 128);
             mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_half[i], 128);
             mbar_init(&bars->p_full[i], 128);
             mbar_init(&bars->o_full[i], 1);
         }
         fence_barrier_init();
     }
-    if (warp == 12)
+    if (warp == 8)
         tc::alloc(tmem_base, kCols);
     tc::fence_before();
     __syncthreads();
@@ -116,6 +141,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
 
     if (warp < 8) {
         // ---- a row per thread -------------------------------------------------
+        regs_up<kRegsRows>();
         const int w = warp >> 2, r = tid & 127, row = 128 * w + r;
         if (w == 0 || two) {
             const bool on = row < live;
@@ -154,6 +180,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
             const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
             const int32_t low = __reduce_min_sync(kFull, limit);
+            // never 0 (a page of zero keys, scale 0): 0 times a masked -infinity is NaN
+            auto factor = [&](float s_k) { return fmaxf(s_k * fac, 0x1p-126f); };
             float m = -1e30f, l = 0.0f;
             for (int j = 0; j < steps; ++j) {
                 if (!mbar_wait(&bars->s_full[w], j & 1, p.wait_limit_ns)) {
@@ -164,25 +192,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 const int32_t key0 = static_cast<int32_t>(kb) + j * kKeys;
                 const bool edge = key0 + kKeys > low;
                 const float4 *sc = scales + (j % kScaleRing) * 8;
+                uint32_t v[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tc::ld32(ts + 32 * c, v[c]);
+                tc::wait_ld();
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (key0 + 32 * c + i >= limit)
+                                v[c][i] = 0xff800000u; // -infinity
+                }
                 float mx = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tc::ld32(ts + 32 * c, v);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float4 f = sc[2 * c + g];
-                        float x = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float y = __uint_as_float(v[16 * g + i]);
-                            if (edge && key0 + 32 * c + 16 * g + i >= limit)
-                                y = -INFINITY;
-                            x = fmaxf(x, y);
-                        }
-                        mx = fmaxf(mx, fmaf(x, f.x * fac, f.y));
-                    }
+                for (int g = 0; g < 8; ++g) {
+                    const uint32_t *y = &v[g >> 1][16 * (g & 1)];
+                    float x = max3(y[0], y[1], y[2]), z = max3(y[3], y[4], y[5]);
+                    x = max3(__float_as_uint(x), y[6], y[7]), z = max3(__float_as_uint(z), y[8], y[9]);
+                    x = max3(__float_as_uint(x), y[10], y[11]), z = max3(__float_as_uint(z), y[12], y[13]);
+                    x = fmaxf(max3(__float_as_uint(x), y[14], y[15]), z);
+                    mx = fmaxf(mx, fmaf(x, factor(sc[g].x), sc[g].y));
                 }
                 if (__any_sync(kFull, mx > m + 8.0f)) {
                     const float mn = fmaxf(m, mx), f = exp2_approx(m - mn);
@@ -204,37 +235,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32], pk[16];
-                    tc::ld32(ts + 32 * c, v);
-                    tc::wait_ld();
+                    uint32_t pk[16];
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const float4 f = sc[2 * c + g];
-                        const float af = f.x * fac, bm = f.y - m;
+                        const float af = factor(f.x), bm = f.y - m;
                         const f32x2 af2 = pack2(af, af), bm2 = pack2(bm, bm);
                         f32x2 sum = pack2(0.0f, 0.0f);
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            const f32x2 x = fma2(pack2(__uint_as_float(v[16 * g + i]), __uint_as_float(v[16 * g + i + 1])),
-                                                 af2, bm2);
-                            float x0 = lo2(x), x1 = hi2(x);
-                            if (edge) {
-                                const int32_t key = key0 + 32 * c + 16 * g + i;
-                                x0 = key >= limit ? -INFINITY : x0;
-                                x1 = key + 1 >= limit ? -INFINITY : x1;
-                            }
-                            x0 = exp2_approx(x0);
-                            x1 = exp2_approx(x1);
+                            const f32x2 x = fma2(
+                                pack2(__uint_as_float(v[c][16 * g + i]), __uint_as_float(v[c][16 * g + i + 1])), af2, bm2);
+                            const float x0 = exp2_approx(lo2(x)), x1 = exp2_approx(hi2(x));
                             sum = add2(sum, pack2(x0, x1));
                             pk[8 * g + i / 2] = pack_f16(x0, x1);
                         }
                         l = fmaf(lo2(sum) + hi2(sum), f.z, l);
                     }
                     tc::st16(ts + 16 * c, pk);
+                    if (c & 1) {
+                        // half of the step's weights: its products may start
+                        tc::wait_st();
+                        tc::fence_before();
+                        mbar_arrive(c == 1 ? &bars->p_half[w] : &bars->p_full[w]);
+                    }
                 }
-                tc::wait_st();
-                tc::fence_before();
-                mbar_arrive(&bars->p_full[w]);
             }
 
             // ---- the row's output -------------------------------------------------
@@ -287,84 +312,133 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 }
             }
         }
-    } else if (warp < 12) {
+    } else if (warp > 8) {
         // ---- codes to fp16 ------------------------------------------------------
-        const int t = tid - 256;
-        constexpr int CPR = D / 16;             // 16-code chunks per key
-        constexpr int RPI = 128 / CPR;          // keys per iteration
-        constexpr int ITERS = kKeys / RPI;      // D = 128: 8 of 16 keys; D = 64: 4 of 32
-        const int kr = t / CPR, cc = t % CPR;
+        regs_down<kRegsRest>();
+        constexpr int CPR = D / 16;            // 16-code chunks per key
+        constexpr int RPW = 32 / CPR;          // keys a warp takes at a time
+        constexpr int GROUPS = kKeys / RPW;    // D = 128: 32 groups of 4 keys; D = 64: 16 of 8
+        constexpr int ITERS = (GROUPS + kConvWarps - 1) / kConvWarps;
+        const int cw = warp - 9, kr = lane / CPR, cc = lane % CPR;
         const int32_t *table = p.batch.table + s * p.batch.table_ld;
         const int items = 2 * steps;
-        uint4 buf[ITERS];
-        auto load = [&](int item) {
-            const int32_t key0 = static_cast<int32_t>(kb) + (item >> 1) * kKeys;
-#pragma unroll
-            for (int it = 0; it < ITERS; ++it) {
-                const int32_t key = key0 + it * RPI + kr;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (key < ke) {
-                    const int32_t id = __ldg(table + (key >> p.cache.log2_page));
-                    if (id >= 0 && id < p.cache.pages) {
-                        const int64_t at = (((static_cast<int64_t>(id) * p.cache.kv_heads + h) << p.cache.log2_page) +
-                                            (key & (p.cache.page - 1))) * D + 16 * cc;
-                        v = __ldg(reinterpret_cast<const uint4 *>(p.cache.codes[item & 1] + at));
-                    } else {
-                        atomicCAS(p.err, 0, kErrPage);
-                    }
-                }
-                buf[it] = v;
+        const uint32_t raw = skv + kRing * S::kStage + 16 * lane;
+        // Group g of this warp's iteration; beyond the last group there is none.
+        auto group = [&](int it) { return it * kConvWarps + cw; };
+        auto page_at = [&](int32_t key) { return key < ke ? __ldg(table + (key >> p.cache.log2_page)) : -2; };
+        auto checked = [&](int32_t id) { // -2: no keys there
+            if (id >= p.cache.pages || id == -1 || id < -2) {
+                atomicCAS(p.err, 0, kErrPage);
+                return -2;
             }
+            return id;
         };
-        if (items > 0)
-            load(0);
+        // Codes travel by asynchronous copies, kRaw items ahead; a thread reads
+        // back only what it copied itself. Keys past the end and pages outside
+        // the cache are zeros. A step's page numbers are loaded a step before
+        // they are used; its K and V share the offsets.
+        int64_t at[ITERS]; // byte offset of this thread's codes, -1: none
+        int32_t next_ids[ITERS];
+        auto load_ids = [&](int j) {
+#pragma unroll
+            for (int it = 0; it < ITERS; ++it)
+                next_ids[it] = group(it) < GROUPS
+                                   ? page_at(static_cast<int32_t>(kb) + j * kKeys + group(it) * RPW + kr) : -2;
+        };
+        auto fetch = [&](int item) {
+            if (item < items) {
+                if ((item & 1) == 0) {
+                    const int32_t key0 = static_cast<int32_t>(kb) + (item >> 1) * kKeys + kr;
+#pragma unroll
+                    for (int it = 0; it < ITERS; ++it) {
+                        const int32_t id = checked(next_ids[it]);
+                        const int32_t slot = (key0 + group(it) * RPW) & (p.cache.page - 1);
+                        at[it] = id < 0 ? -1 : (((static_cast<int64_t>(id) * p.cache.kv_heads + h) << p.cache.log2_page) +
+                                                slot) * D + 16 * cc;
+                    }
+                    load_ids((item >> 1) + 1);
+                }
+                const uint8_t *codes = p.cache.codes[item & 1];
+#pragma unroll
+                for (int it = 0; it < ITERS; ++it)
+                    if (group(it) < GROUPS)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         raw + (item % kRaw) * S::kCodes + group(it) * 512),
+                                     "l"(codes + (at[it] < 0 ? 0 : at[it])), "r"(at[it] < 0 ? 0 : 16));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // s_k and s_v of 16-key group `lane` of a step (lanes 0-7 of the first
+        // warp), a step ahead; s_v < 0: no keys
+        const bool scaler = cw == 0 && lane < 8;
+        float s_k = 0.0f, s_v = -1.0f;
+        int32_t scale_id = -2;
+        auto load_scale_id = [&](int j) {
+            if (scaler)
+                scale_id = page_at(static_cast<int32_t>(kb) + j * kKeys + 16 * lane);
+        };
+        auto load_scales = [&] {
+            const bool on = scale_id >= 0 && scale_id < p.cache.pages;
+            const int64_t ph = on ? static_cast<int64_t>(scale_id) * p.cache.kv_heads + h : 0;
+            s_k = on ? __ldg(p.cache.scales[0] + ph) : 0.0f;
+            s_v = on ? __ldg(p.cache.scales[1] + ph) : -1.0f;
+        };
+        load_ids(0);
+        load_scale_id(0);
+        load_scales();
+        load_scale_id(1);
+        for (int item = 0; item < kRaw; ++item)
+            fetch(item);
         for (int item = 0; item < items; ++item) {
             const int st = item % kRing;
             if (item >= kRing && !mbar_wait(&bars->kv_empty[st], (item / kRing - 1) & 1, p.wait_limit_ns)) {
                 failed = true;
                 break;
             }
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
             const uint32_t dst = skv + st * S::kStage;
+            uint32_t u[ITERS][4];
+#pragma unroll
+            for (int it = 0; it < ITERS; ++it)
+                if (group(it) < GROUPS)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(u[it][0]), "=r"(u[it][1]), "=r"(u[it][2]), "=r"(u[it][3])
+                                 : "r"(raw + (item % kRaw) * S::kCodes + group(it) * 512));
 #pragma unroll
             for (int it = 0; it < ITERS; ++it) {
-                const uint32_t u[4] = {buf[it].x, buf[it].y, buf[it].z, buf[it].w};
                 uint32_t f[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    codes4_to_f16<FP8>(u[i], f[2 * i], f[2 * i + 1]);
+                    codes4_to_f16<FP8>(u[it][i], f[2 * i], f[2 * i + 1]);
                 // the second half of a row's lanes swaps its two stores: all 8 lanes of a
                 // store phase then hit different banks
-                const int r = it * RPI + kr, odd = (cc >> 2) & 1;
-                const uint32_t a0 = dst + chunk_at<D>(r, 2 * cc), a1 = dst + chunk_at<D>(r, 2 * cc + 1);
-                if (odd) {
-                    sts16(a1, f[4], f[5], f[6], f[7]);
-                    sts16(a0, f[0], f[1], f[2], f[3]);
-                } else {
-                    sts16(a0, f[0], f[1], f[2], f[3]);
-                    sts16(a1, f[4], f[5], f[6], f[7]);
+                const int r = group(it) * RPW + kr;
+                const bool odd = (cc & 4) != 0;
+                const uint32_t a0 = dst + chunk_at<D>(r, 2 * cc), a1 = a0 ^ 16;
+                if (group(it) < GROUPS) {
+                    sts16(odd ? a1 : a0, odd ? f[4] : f[0], odd ? f[5] : f[1], odd ? f[6] : f[2], odd ? f[7] : f[3]);
+                    sts16(odd ? a0 : a1, odd ? f[0] : f[4], odd ? f[1] : f[5], odd ? f[2] : f[6], odd ? f[3] : f[7]);
                 }
             }
-            if ((item & 1) == 0 && t < 8) {
-                // the scales of the step's 16-key groups, with its K
-                const int j = item >> 1;
-                const int32_t key = static_cast<int32_t>(kb) + j * kKeys + 16 * t;
-                float4 f = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
-                if (key < ke) {
-                    const int32_t id = __ldg(table + (key >> p.cache.log2_page));
-                    if (id >= 0 && id < p.cache.pages) {
-                        const int64_t ph = static_cast<int64_t>(id) * p.cache.kv_heads + h;
-                        const float sv = fmaxf(__ldg(p.cache.scales[1] + ph), 0x1p-100f);
-                        f = make_float4(__ldg(p.cache.scales[0] + ph), log2f(sv), __frcp_rn(sv), 0.0f);
-                    }
-                }
-                scales[(j % kScaleRing) * 8 + t] = f;
+            if ((item & 1) == 0 && scaler) {
+                // with a step's K, the scales of its 16-key groups
+                const float sv = fmaxf(s_v, 0x1p-100f);
+                scales[(item / 2 % kScaleRing) * 8 + lane] =
+                    s_v < 0.0f ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+                               : make_float4(s_k, log2f(sv), __frcp_rn(sv), 0.0f);
             }
             tc::fence_proxy();
             mbar_arrive(&bars->kv_full[st]);
-            if (item + 1 < items)
-                load(item + 1);
+            if ((item & 1) == 0 && scaler) {
+                load_scales();
+                load_scale_id((item >> 1) + 2);
+            }
+            fetch(item + kRaw);
         }
-    } else if (warp == 12 && lane == 0 && steps > 0) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        regs_down<kRegsRest>();
+        if (lane == 0 && steps > 0) {
         // ---- MMAs -----------------------------------------------------------------
         constexpr uint32_t kIS = f16_idesc(kKeys, false), kIO = f16_idesc(D, true);
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -381,10 +455,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             }
             tc::commit(&bars->s_full[w]);
         };
-        auto values = [&](int w, int st, int j) {
+        // the first or second half of a step's keys
+        auto values = [&](int w, int st, int j, int half) {
             const uint32_t v = skv + st * S::kStage;
 #pragma unroll
-            for (int ks = 0; ks < kKeys / 16; ++ks)
+            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
                 tc::mma_f16_ta(tmem + 256 + 128 * w, tmem + 128 * w + 8 * ks, tc::desc_mnmajor(v + ks * 2048, S::kAtom), kIO,
                                j > 0 || ks > 0);
         };
@@ -401,10 +476,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             const int vi = 2 * j + 1, ki = 2 * j + 2, vs = vi % kRing, ks = ki % kRing;
             wait(&bars->kv_full[vs], (vi / kRing) & 1);
             for (int w = 0; w < tiles; ++w) {
+                if (!wait(&bars->p_half[w], j & 1))
+                    break;
+                tc::fence_after();
+                values(w, vs, j, 0);
                 if (!wait(&bars->p_full[w], j & 1))
                     break;
                 tc::fence_after();
-                values(w, vs, j);
+                values(w, vs, j, 1);
                 if (w == tiles - 1)
                     tc::commit(&bars->kv_empty[vs]);
                 if (j + 1 < steps) {
@@ -421,13 +500,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             tc::commit(&bars->o_full[w]);
         // every MMA has finished before the tensor memory goes
         (void)mbar_wait(&bars->o_full[0], 0, p.wait_limit_ns);
+        }
     }
     if (failed)
         atomicCAS(p.err, 0, kErrAttendWait);
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 8) {
         tc::fence_after();
         tc::dealloc(tmem, kCols);
     }
