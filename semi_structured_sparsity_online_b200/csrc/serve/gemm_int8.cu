@@ -4,14 +4,25 @@
 //   y[t][c] = RN(RN(RN(sum_k a[t][k] b[c][k]) s_a[t]) s_b[c])
 //
 // a: token rows, b: channel rows (a weight), both as ss24_quantize_int writes
-// them with bits 8 and group 0. The sum is exact in 32-bit integers for k <=
-// 133,144 (127^2 k < 2^31); it is rounded once to binary32 and once by each
-// scale, and once more where y is bf16.
+// them with bits 8 and group 0. The sum is exact in 32-bit integers (128^2 k <
+// 2^31); it is rounded once to binary32 and once by each scale, and once more
+// where y is bf16.
 //
-// Roles. The channels are the MMA's M (128 rows), the tokens its N: a token
-// count that is small costs a narrow MMA, not an idle one, and a thread's
+// Roles. The channels are the MMA's M (128 rows a CTA), the tokens its N: a
+// small token count costs a narrow MMA, not an idle one, and a thread's
 // accumulator row is one channel, so that the 32 lanes of a warp write 32
 // consecutive channels of a token (whole sectors, any n and ldy).
+//
+// Two kernels:
+//   pair   256 x 256 tiles by pairs of CTAs, persistent, two accumulators in
+//          tensor memory. A CTA brings 128 channel rows and 128 token rows and
+//          the pair's MMA uses all four halves: 64 bytes a clock to each SM at
+//          the MMA's full rate, where one CTA's own 128 x 256 tile needs 96
+//          (and reads 96 of the 128 shared memory gives beside that).
+//   split  128 channels x 16 ... 128 tokens by one CTA, the k axis split over a
+//          cluster of up to 8 CTAs and joined through their shared memory: few
+//          tokens, where the weight's bytes bound the call and tiles of all of
+//          k would leave most SMs idle.
 #include "serve.cuh"
 #include "tcgen05.cuh"
 
@@ -19,41 +30,231 @@ namespace ss24 {
 
 namespace {
 
-constexpr int kBM = 128;      // channels per tile
-constexpr int kBK = 128;      // k per stage (bytes)
-constexpr int kThreadsG = 128;
+constexpr int kBM = 128; // channels per CTA
+constexpr int kBK = 128; // k per stage (bytes)
 
-template <int BN> struct Shape {
-    static constexpr int kStagesG = BN >= 256 ? 4 : 6;
-    static constexpr uint32_t kABytes = kBM * kBK, kBBytes = BN * kBK;
-    static constexpr uint32_t kStage = kABytes + kBBytes;
-    static constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
-    static constexpr size_t kSmem = kStagesG * kStage + 1024 + 256 + 4 * BN;
+// s32 accumulator, s8 x s8, both K-major
+__host__ __device__ constexpr uint32_t i8_idesc(int m, int n)
+{
+    return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p)
+{
+    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+__device__ __forceinline__ void store_y(const GemmInt8Params &p, int64_t t, int64_t c, uint32_t acc, float sa, float sb)
+{
+    const float r = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc)), sa), sb);
+    if (p.y_f32)
+        static_cast<float *>(p.y)[t * p.ldy + c] = r;
+    else
+        static_cast<__nv_bfloat16 *>(p.y)[t * p.ldy + c] = __float2bfloat16_rn(r);
+}
+
+// ---------------------------------------------------------------------------
+// pair: 256 channels x 256 tokens by two CTAs
+// ---------------------------------------------------------------------------
+
+constexpr int kPairThreads = 256; // warp 0: loads, warp 1: MMAs, warps 4-7: epilogue
+constexpr int kPairN = 256, kPairStages = 6;
+constexpr uint32_t kPairStage = 2 * kBM * kBK; // 128 channel rows, 128 token rows
+constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + 512;
+constexpr int kRaster = 8; // token tiles served together
+
+struct PairBars {
+    uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2];
 };
 
-// s32 accumulator, s8 x s8, both K-major, M = 128, N = BN
-template <int BN>
-constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(BN >> 3) << 17) |
-                            (static_cast<uint32_t>(kBM >> 4) << 24);
+// Tile i of the persistent order: kRaster token tiles by all channel tiles at a
+// time, so that the tiles in flight share rows of both operands in L2.
+__device__ __forceinline__ void pair_tile(int64_t i, int64_t tt, int64_t ct, int64_t *t, int64_t *c)
+{
+    const int64_t band = i / (kRaster * ct), r = i - band * kRaster * ct;
+    const int64_t height = tt - band * kRaster < kRaster ? tt - band * kRaster : kRaster;
+    *t = band * kRaster + r % height;
+    *c = r / height;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    gemm_int8_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                          const GemmInt8Params p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *stages = align1024(smem_raw);
+    PairBars *bars = reinterpret_cast<PairBars *>(stages + kPairStages * kPairStage);
+    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(bars + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int64_t tt = (p.m + kPairN - 1) / kPairN, ct = (p.n + 2 * kBM - 1) / (2 * kBM), tiles = tt * ct;
+    const int nk = static_cast<int>((p.k + kBK - 1) / kBK);
+
+    if (tid == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars->acc_full[s], 1);
+            mbar_init(&bars->acc_empty[s], 8); // the epilogue warps of both CTAs
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1)
+        tc::alloc_pair(tmem_base, 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_base;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    bool failed = false;
+
+    if (warp == 0 && lane == 0) {
+        int it = 0, phase = 0;
+        int64_t issued = 0;
+        for (int64_t i = pair; i < tiles && !failed; i += pairs) {
+            int64_t t, c;
+            pair_tile(i, tt, ct, &t, &c);
+            const int32_t row_w = static_cast<int32_t>(c * 2 * kBM + rank * kBM);
+            const int32_t row_x = static_cast<int32_t>(t * kPairN + rank * kBM);
+            for (int kt = 0; kt < nk; ++kt) {
+                if (!mbar_wait(&bars->empty[it], phase ^ 1, p.wait_limit_ns)) {
+                    failed = true;
+                    break;
+                }
+                const uint32_t at = smem_u32(stages + it * kPairStage);
+                if (rank == 0)
+                    mbar_arrive_expect_tx(&bars->full[it], 2 * kPairStage);
+                const uint32_t bar = tc::cluster_addr(smem_u32(&bars->full[it]), 0);
+                tc::tma_box_pair(at, &map_w, kt * kBK, row_w, bar);
+                tc::tma_box_pair(at + kBM * kBK, &map_x, kt * kBK, row_x, bar);
+                ++issued;
+                if (++it == kPairStages)
+                    it = 0, phase ^= 1;
+            }
+        }
+        // the stages' last readers: a CTA leaves only after its copies have landed
+        for (int64_t j = issued > kPairStages ? issued - kPairStages : 0; j < issued; ++j)
+            if (!mbar_wait(&bars->empty[j % kPairStages], (j / kPairStages) & 1, p.wait_limit_ns))
+                failed = true;
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        constexpr uint32_t kI = i8_idesc(256, kPairN);
+        int it = 0, phase = 0, n = 0;
+        for (int64_t i = pair; i < tiles && !failed; i += pairs, ++n) {
+            const int a = n & 1;
+            if (!mbar_wait(&bars->acc_empty[a], ((n >> 1) & 1) ^ 1, p.wait_limit_ns)) {
+                failed = true;
+                break;
+            }
+            tc::fence_after();
+            for (int kt = 0; kt < nk; ++kt) {
+                if (!mbar_wait(&bars->full[it], phase, p.wait_limit_ns)) {
+                    failed = true;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t at = smem_u32(stages + it * kPairStage);
+#pragma unroll
+                for (int j = 0; j < kBK / 32; ++j)
+                    tc::mma_i8_pair(tmem + a * kPairN, tc::desc_kmajor(at + 32 * j),
+                                    tc::desc_kmajor(at + kBM * kBK + 32 * j), kI, (kt | j) != 0);
+                tc::commit_pair(&bars->empty[it]);
+                if (++it == kPairStages)
+                    it = 0, phase ^= 1;
+            }
+            tc::commit_pair(&bars->acc_full[a]);
+        }
+    } else if (warp >= 4) {
+        const int w = warp & 3;
+        int n = 0;
+        for (int64_t i = pair; i < tiles; i += pairs, ++n) {
+            int64_t t, c;
+            pair_tile(i, tt, ct, &t, &c);
+            const int a = n & 1;
+            if (!mbar_wait(&bars->acc_full[a], (n >> 1) & 1, p.wait_limit_ns)) {
+                failed = true;
+                break;
+            }
+            tc::fence_after();
+            const int64_t ch = c * 2 * kBM + rank * kBM + 32 * w + lane;
+            const bool on = ch < p.n;
+            const float sb = on ? p.b_scale[ch] : 0.0f;
+            const int64_t t0 = t * kPairN;
+            const int cols = static_cast<int>(p.m - t0 < kPairN ? p.m - t0 : kPairN);
+            const uint32_t at = tmem + (static_cast<uint32_t>(32 * w) << 16) + a * kPairN;
+#pragma unroll 1
+            for (int j0 = 0; j0 < cols; j0 += 32) {
+                uint32_t v[32];
+                __syncwarp();
+                tc::ld32(at + j0, v);
+                const float sa = t0 + j0 + lane < p.m ? __ldg(p.a_scale + t0 + j0 + lane) : 0.0f;
+                tc::wait_ld();
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                    const float s = __shfl_sync(kFull, sa, q);
+                    if (on && j0 + q < cols)
+                        store_y(p, t0 + j0 + q, ch, v[q], s, sb);
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::arrive_cluster(tc::cluster_addr(smem_u32(&bars->acc_empty[a]), 0));
+        }
+    }
+    if (failed)
+        atomicCAS(p.err, 0, kErrGemmWait);
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::dealloc_pair(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// split: 128 channels x BN tokens, k over the CTAs of a cluster
+// ---------------------------------------------------------------------------
+
+constexpr int kSplitThreads = 128;
+
+template <int BN> struct Split {
+    static constexpr int kStages = BN <= 64 ? 4 : 6;
+    static constexpr int kPerSm = BN <= 64 ? 2 : 1; // CTAs that fit an SM's shared memory
+    static constexpr uint32_t kStage = (kBM + BN) * kBK;
+    static constexpr uint32_t kCols = BN < 32 ? 32 : BN;
+    static constexpr size_t kSmem = 1024 + kStages * kStage + 128 + 4 * BN;
+    static_assert(kStages * kStage >= 4 * kBM * BN, "the stages hold a CTA's sums");
+};
 
 template <int BN>
-__global__ void __launch_bounds__(kThreadsG, 1)
-    gemm_int8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                     const GemmInt8Params p)
+__global__ void __launch_bounds__(kSplitThreads)
+    gemm_int8_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                           const GemmInt8Params p, const int32_t parts)
 {
-    using S = Shape<BN>;
-    constexpr int STAGES = S::kStagesG;
+    using S = Split<BN>;
+    constexpr int STAGES = S::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *stages = align1024(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(stages + STAGES * S::kStage);
     uint64_t *empty = full + STAGES;
     uint64_t *accbar = empty + STAGES;
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(accbar + 1);
-    float *sa = reinterpret_cast<float *>(accbar + 4);
+    float *sa = reinterpret_cast<float *>(accbar + 2);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kBM, t0 = static_cast<int64_t>(blockIdx.y) * BN;
-    const int nk = static_cast<int>((p.k + kBK - 1) / kBK);
+    const int rank = static_cast<int>(blockIdx.x % parts);
+    const int64_t ct = (p.n + kBM - 1) / kBM, tile = blockIdx.x / parts;
+    const int64_t c0 = tile % ct * kBM, t0 = tile / ct * BN;
+    const int64_t nk = (p.k + kBK - 1) / kBK;
+    const int kt0 = static_cast<int>(nk * rank / parts), kt1 = static_cast<int>(nk * (rank + 1) / parts);
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -63,86 +264,112 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         mbar_init(accbar, 1);
         fence_barrier_init();
     }
-    if (warp == 0)
-        tc::alloc(tmem_base, S::kTmemCols);
+    if (warp == 1)
+        tc::alloc(tmem_base, S::kCols);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *tmem_base;
+    grid_dependents_launch();
     grid_dependency_wait();
+    bool failed = false;
 
     if (warp == 0 && lane == 0) {
         int issued = 0;
-        bool failed = false;
-        for (int kt = 0; kt < nk; ++kt) {
-            const int s = kt % STAGES;
-            if (kt >= STAGES && !mbar_wait(&empty[s], ((kt / STAGES) - 1) & 1, p.wait_limit_ns)) {
+        for (int kt = kt0; kt < kt1; ++kt, ++issued) {
+            const int s = issued % STAGES;
+            if (issued >= STAGES && !mbar_wait(&empty[s], (issued / STAGES - 1) & 1, p.wait_limit_ns)) {
                 failed = true;
                 break;
             }
             const uint32_t at = smem_u32(stages + s * S::kStage);
             mbar_arrive_expect_tx(&full[s], S::kStage);
             tc::tma_box(at, &map_w, kt * kBK, static_cast<int32_t>(c0), &full[s]);
-            tc::tma_box(at + S::kABytes, &map_x, kt * kBK, static_cast<int32_t>(t0), &full[s]);
-            ++issued;
+            tc::tma_box(at + kBM * kBK, &map_x, kt * kBK, static_cast<int32_t>(t0), &full[s]);
         }
-        if (failed) {
-            atomicCAS(p.err, 0, kErrGemmWait);
-            // the copies already issued land before the CTA can exit
-            for (int kt = issued > STAGES ? issued - STAGES : 0; kt < issued; ++kt)
-                (void)mbar_wait(&full[kt % STAGES], (kt / STAGES) & 1, p.wait_limit_ns);
-        }
+        if (failed) // the copies already issued land before the CTA can exit
+            for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+                (void)mbar_wait(&full[i % STAGES], (i / STAGES) & 1, p.wait_limit_ns);
     } else if (warp == 1 && lane == 0) {
-        for (int kt = 0; kt < nk; ++kt) {
-            const int s = kt % STAGES;
-            if (!mbar_wait(&full[s], (kt / STAGES) & 1, p.wait_limit_ns)) {
-                atomicCAS(p.err, 0, kErrGemmWait);
+        constexpr uint32_t kI = i8_idesc(128, BN);
+        for (int i = 0; i < kt1 - kt0; ++i) {
+            const int s = i % STAGES;
+            if (!mbar_wait(&full[s], (i / STAGES) & 1, p.wait_limit_ns)) {
+                failed = true;
                 break;
             }
             tc::fence_after();
             const uint32_t at = smem_u32(stages + s * S::kStage);
 #pragma unroll
             for (int j = 0; j < kBK / 32; ++j)
-                tc::mma_i8(tmem, tc::desc_kmajor(at + 32 * j), tc::desc_kmajor(at + S::kABytes + 32 * j), kIdesc<BN>,
-                           (kt | j) != 0 ? 1u : 0u);
+                tc::mma_i8(tmem, tc::desc_kmajor(at + 32 * j), tc::desc_kmajor(at + kBM * kBK + 32 * j), kI, (i | j) != 0);
             tc::commit(&empty[s]);
         }
         tc::commit(accbar);
     }
     __syncwarp();
-    for (int i = tid; i < BN; i += kThreadsG)
-        sa[i] = t0 + i < p.m ? p.a_scale[t0 + i] : 0.0f;
-    __syncthreads();
-    if (!mbar_wait(accbar, 0, p.wait_limit_ns) && lane == 0)
-        atomicCAS(p.err, 0, kErrGemmWait);
-    tc::fence_after();
-
+    const int cols = static_cast<int>(p.m - t0 < BN ? p.m - t0 : BN);
+    for (int i = tid; i < cols; i += kSplitThreads)
+        sa[i] = p.a_scale[t0 + i];
     const int64_t c = c0 + 32 * warp + lane;
-    const float sb = c < p.n ? p.b_scale[c] : 0.0f;
+    const bool on = c < p.n;
+    const float sb = on ? p.b_scale[c] : 0.0f;
+    __syncthreads();
+    if (!mbar_wait(accbar, 0, p.wait_limit_ns))
+        failed = true;
+    tc::fence_after();
+    const uint32_t acc = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    if (parts == 1) {
 #pragma unroll 1
-    for (int j0 = 0; j0 < BN; j0 += 16) {
-        if (t0 + j0 >= p.m)
-            break;
-        uint32_t v[16];
-        tc::ld16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + j0, v);
-        tc::wait_ld();
+        for (int j0 = 0; j0 < cols; j0 += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tc::ld16(acc + j0, v);
+            tc::wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int64_t t = t0 + j0 + i;
-            if (t < p.m && c < p.n) {
-                const float r = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(v[i])), sa[j0 + i]), sb);
-                if (p.y_f32)
-                    static_cast<float *>(p.y)[t * p.ldy + c] = r;
-                else
-                    static_cast<__nv_bfloat16 *>(p.y)[t * p.ldy + c] = __float2bfloat16_rn(r);
-            }
+            for (int i = 0; i < 16; ++i)
+                if (on && j0 + i < cols)
+                    store_y(p, t0 + j0 + i, c, v[i], sa[j0 + i], sb);
         }
+    } else {
+        // this part's sums over the stages (all read by now): column j, channel
+        // tid at 4 (128 j + tid); then each CTA joins its share of the columns
+        const uint32_t sums = smem_u32(stages) + 4 * tid;
+#pragma unroll 1
+        for (int j0 = 0; j0 < cols; j0 += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tc::ld16(acc + j0, v);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(sums + 512 * (j0 + i)), "r"(v[i]) : "memory");
+        }
+        tc::cluster_sync();
+        const int share = (cols + parts - 1) / parts;
+        const int j1 = (rank + 1) * share < cols ? (rank + 1) * share : cols;
+        for (int j = rank * share; j < j1; ++j) {
+            int sum = 0;
+            for (int r = 0; r < parts; ++r) {
+                int x;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                             : "=r"(x)
+                             : "r"(tc::cluster_addr(sums + 512 * j, r))
+                             : "memory");
+                sum += x;
+            }
+            if (on)
+                store_y(p, t0 + j, c, static_cast<uint32_t>(sum), sa[j], sb);
+        }
+        tc::cluster_sync(); // a CTA's sums stay until the others have read them
     }
+    if (failed)
+        atomicCAS(p.err, 0, kErrGemmWait);
     tc::fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         tc::fence_after();
-        tc::dealloc(tmem, S::kTmemCols);
+        tc::dealloc(tmem, S::kCols);
     }
 }
 
@@ -167,41 +394,76 @@ bool encode_rows(CUtensorMap *map, const int8_t *base, int64_t rows, int64_t k, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN> cudaError_t launch_bn(const GemmInt8Params &p, cudaStream_t stream)
+template <typename K, typename... A>
+cudaError_t launch_gemm(K kern, size_t smem, int64_t grid, int threads, int cluster, cudaStream_t stream, A... args)
 {
-    using S = Shape<BN>;
-    CUtensorMap mw, mx;
-    if (!encode_rows(&mw, p.b, p.n, p.k, kBM) || !encode_rows(&mx, p.a, p.m, p.k, BN))
-        return cudaErrorInvalidValue;
-    auto kern = gemm_int8_kernel<BN>;
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.n + kBM - 1) / kBM), static_cast<unsigned>((p.m + BN - 1) / BN));
-    cfg.blockDim = dim3(kThreadsG);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kSms = 148;
+
+template <int BN> cudaError_t launch_split(const GemmInt8Params &p, cudaStream_t stream)
+{
+    CUtensorMap mw, mx;
+    if (!encode_rows(&mw, p.b, p.n, p.k, kBM) || !encode_rows(&mx, p.a, p.m, p.k, BN))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = ceil_div(p.n, kBM) * ceil_div(p.m, BN), nk = ceil_div(p.k, kBK);
+    if (tiles > INT32_MAX / 8)
+        return cudaErrorInvalidValue;
+    // parts of k: doubled while all CTAs still run at once and each keeps at
+    // least two stages of work
+    int parts = 1;
+    while (parts < 8 && tiles * parts * 2 <= Split<BN>::kPerSm * kSms && nk >= 4 * parts)
+        parts *= 2;
+    return launch_gemm(gemm_int8_split_kernel<BN>, Split<BN>::kSmem, tiles * parts, kSplitThreads, parts, stream, mw, mx,
+                       p, static_cast<int32_t>(parts));
+}
+
+cudaError_t launch_pair(const GemmInt8Params &p, cudaStream_t stream)
+{
+    CUtensorMap mw, mx;
+    if (!encode_rows(&mw, p.b, p.n, p.k, kBM) || !encode_rows(&mx, p.a, p.m, p.k, kBM))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = ceil_div(p.n, 2 * kBM) * ceil_div(p.m, kPairN);
+    const int64_t pairs = tiles < kSms / 2 ? tiles : kSms / 2;
+    return launch_gemm(gemm_int8_pair_kernel, kPairSmem, 2 * pairs, kPairThreads, 1, stream, mw, mx, p);
 }
 
 } // namespace
 
 cudaError_t launch_gemm_int8(const GemmInt8Params &p, cudaStream_t stream)
 {
+    // pairs where their tiles occupy a good part of the SMs
+    if (p.m > 128 && ceil_div(p.n, 2 * kBM) * ceil_div(p.m, kPairN) >= kSms / 4)
+        return launch_pair(p, stream);
     if (p.m <= 16)
-        return launch_bn<16>(p, stream);
+        return launch_split<16>(p, stream);
+    if (p.m <= 32)
+        return launch_split<32>(p, stream);
     if (p.m <= 64)
-        return launch_bn<64>(p, stream);
-    if (p.m <= 128)
-        return launch_bn<128>(p, stream);
-    return launch_bn<256>(p, stream);
+        return launch_split<64>(p, stream);
+    return launch_split<128>(p, stream);
 }
 
 } // namespace ss24
