@@ -45,23 +45,23 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
     return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-__device__ __forceinline__ void store_y(const GemmInt8Params &p, int64_t t, int64_t c, uint32_t acc, float sa, float sb)
+__device__ __forceinline__ void store_y(float *y, uint32_t acc, float sa, float sb)
 {
-    const float r = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc)), sa), sb);
-    if (p.y_f32)
-        static_cast<float *>(p.y)[t * p.ldy + c] = r;
-    else
-        static_cast<__nv_bfloat16 *>(p.y)[t * p.ldy + c] = __float2bfloat16_rn(r);
+    *y = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc)), sa), sb);
+}
+__device__ __forceinline__ void store_y(__nv_bfloat16 *y, uint32_t acc, float sa, float sb)
+{
+    *y = __float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(acc)), sa), sb));
 }
 
 // ---------------------------------------------------------------------------
 // pair: 256 channels x 256 tokens by two CTAs
 // ---------------------------------------------------------------------------
 
-constexpr int kPairThreads = 256; // warp 0: loads, warp 1: MMAs, warps 4-7: epilogue
+constexpr int kPairThreads = 384; // warp 0: loads, warp 1: MMAs, warps 4-11: epilogue
 constexpr int kPairN = 256, kPairStages = 6;
 constexpr uint32_t kPairStage = 2 * kBM * kBK; // 128 channel rows, 128 token rows
-constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + 512;
+constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + 512 + 2 * kPairN * 4;
 constexpr int kRaster = 8; // token tiles served together
 
 struct PairBars {
@@ -78,6 +78,7 @@ __device__ __forceinline__ void pair_tile(int64_t i, int64_t tt, int64_t ct, int
     *c = r / height;
 }
 
+template <typename Y>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     gemm_int8_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                           const GemmInt8Params p)
@@ -86,6 +87,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint8_t *stages = align1024(smem_raw);
     PairBars *bars = reinterpret_cast<PairBars *>(stages + kPairStages * kPairStage);
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(bars + 1);
+    float *sa = reinterpret_cast<float *>(stages + kPairStages * kPairStage + 512); // [2][kPairN]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = tc::cluster_rank();
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -99,7 +101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars->acc_full[s], 1);
-            mbar_init(&bars->acc_empty[s], 8); // the epilogue warps of both CTAs
+            mbar_init(&bars->acc_empty[s], 16); // the epilogue warps of both CTAs
         }
         fence_barrier_init();
     }
@@ -170,36 +172,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc::commit_pair(&bars->acc_full[a]);
         }
     } else if (warp >= 4) {
-        const int w = warp & 3;
+        // warps 4-7 take the tile's first 128 tokens, warps 8-11 the others
+        const int w = warp & 3, half = (warp - 4) >> 2;
         int n = 0;
         for (int64_t i = pair; i < tiles; i += pairs, ++n) {
             int64_t t, c;
             pair_tile(i, tt, ct, &t, &c);
             const int a = n & 1;
+            const int64_t ch = c * 2 * kBM + rank * kBM + 32 * w + lane, t0 = t * kPairN + half * 128;
+            const bool on = ch < p.n;
+            const float sb = on ? __ldg(p.b_scale + ch) : 0.0f;
+            float *const s = sa + a * kPairN + half * 128;
+            const int64_t own = t0 + 32 * w + lane;
+            s[32 * w + lane] = own < p.m ? __ldg(p.a_scale + own) : 0.0f;
+            named_barrier_sync(1 + half, 128);
             if (!mbar_wait(&bars->acc_full[a], (n >> 1) & 1, p.wait_limit_ns)) {
                 failed = true;
                 break;
             }
             tc::fence_after();
-            const int64_t ch = c * 2 * kBM + rank * kBM + 32 * w + lane;
-            const bool on = ch < p.n;
-            const float sb = on ? p.b_scale[ch] : 0.0f;
-            const int64_t t0 = t * kPairN;
-            const int cols = static_cast<int>(p.m - t0 < kPairN ? p.m - t0 : kPairN);
-            const uint32_t at = tmem + (static_cast<uint32_t>(32 * w) << 16) + a * kPairN;
+            const int64_t room = p.m - t0;
+            const int cols = static_cast<int>(room < 0 ? 0 : room < 128 ? room : 128);
+            const uint32_t at = tmem + (static_cast<uint32_t>(32 * w) << 16) + a * kPairN + half * 128;
+            Y *y = static_cast<Y *>(p.y) + t0 * p.ldy + ch;
 #pragma unroll 1
             for (int j0 = 0; j0 < cols; j0 += 32) {
                 uint32_t v[32];
                 __syncwarp();
                 tc::ld32(at + j0, v);
-                const float sa = t0 + j0 + lane < p.m ? __ldg(p.a_scale + t0 + j0 + lane) : 0.0f;
                 tc::wait_ld();
+                if (j0 + 32 <= cols) {
+                    if (on) {
 #pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                    const float s = __shfl_sync(kFull, sa, q);
-                    if (on && j0 + q < cols)
-                        store_y(p, t0 + j0 + q, ch, v[q], s, sb);
+                        for (int q = 0; q < 32; ++q)
+                            store_y(y + q * p.ldy, v[q], s[j0 + q], sb);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 32; ++q)
+                        if (on && j0 + q < cols)
+                            store_y(y + q * p.ldy, v[q], s[j0 + q], sb);
                 }
+                y += 32 * p.ldy;
             }
             tc::fence_before();
             __syncwarp();
@@ -234,7 +248,7 @@ template <int BN> struct Split {
     static_assert(kStages * kStage >= 4 * kBM * BN, "the stages hold a CTA's sums");
 };
 
-template <int BN>
+template <int BN, typename Y>
 __global__ void __launch_bounds__(kSplitThreads)
     gemm_int8_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                            const GemmInt8Params p, const int32_t parts)
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (on && j0 + i < cols)
-                    store_y(p, t0 + j0 + i, c, v[i], sa[j0 + i], sb);
+                    store_y(static_cast<Y *>(p.y) + (t0 + j0 + i) * p.ldy + c, v[i], sa[j0 + i], sb);
         }
     } else {
         // this part's sums over the stages (all read by now): column j, channel
@@ -359,7 +373,7 @@ __global__ void __launch_bounds__(kSplitThreads)
                 sum += x;
             }
             if (on)
-                store_y(p, t0 + j, c, static_cast<uint32_t>(sum), sa[j], sb);
+                store_y(static_cast<Y *>(p.y) + (t0 + j) * p.ldy + c, static_cast<uint32_t>(sum), sa[j], sb);
         }
         tc::cluster_sync(); // a CTA's sums stay until the others have read them
     }
@@ -436,8 +450,9 @@ template <int BN> cudaError_t launch_split(const GemmInt8Params &p, cudaStream_t
     int parts = 1;
     while (parts < 8 && tiles * parts * 2 <= Split<BN>::kPerSm * kSms && nk >= 4 * parts)
         parts *= 2;
-    return launch_gemm(gemm_int8_split_kernel<BN>, Split<BN>::kSmem, tiles * parts, kSplitThreads, parts, stream, mw, mx,
-                       p, static_cast<int32_t>(parts));
+    return launch_gemm(p.y_f32 ? gemm_int8_split_kernel<BN, float> : gemm_int8_split_kernel<BN, __nv_bfloat16>,
+                       Split<BN>::kSmem, tiles * parts, kSplitThreads, parts, stream, mw, mx, p,
+                       static_cast<int32_t>(parts));
 }
 
 cudaError_t launch_pair(const GemmInt8Params &p, cudaStream_t stream)
@@ -447,7 +462,8 @@ cudaError_t launch_pair(const GemmInt8Params &p, cudaStream_t stream)
         return cudaErrorInvalidValue;
     const int64_t tiles = ceil_div(p.n, 2 * kBM) * ceil_div(p.m, kPairN);
     const int64_t pairs = tiles < kSms / 2 ? tiles : kSms / 2;
-    return launch_gemm(gemm_int8_pair_kernel, kPairSmem, 2 * pairs, kPairThreads, 1, stream, mw, mx, p);
+    return launch_gemm(p.y_f32 ? gemm_int8_pair_kernel<float> : gemm_int8_pair_kernel<__nv_bfloat16>, kPairSmem, 2 * pairs,
+                       kPairThreads, 1, stream, mw, mx, p);
 }
 
 } // namespace
