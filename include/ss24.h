@@ -560,7 +560,7 @@ typedef struct {
     float *k_scales, *v_scales; /* [pages][kv_heads]                                          */
     int32_t kind;               /* SS24_FMT_INT (8 bits) or SS24_FMT_FP8_E4M3                 */
     int32_t page;               /* tokens per page: 16, 32, 64 or 128                         */
-    int64_t pages;
+    int64_t pages;              /* pages * kv_heads * page below 2^31                         */
     int32_t kv_heads;           /* 1 .. 1024                                                  */
     int32_t head_dim;           /* 64 or 128                                                  */
 } ss24_kv_cache;

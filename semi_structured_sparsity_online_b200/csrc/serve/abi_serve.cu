@@ -29,7 +29,7 @@ ss24_status check_cache(const ss24_kv_cache *c, KvCache *out)
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
         return SS24_ERR_SHAPE;
     if ((c->head_dim != 64 && c->head_dim != 128) || c->kv_heads < 1 || c->kv_heads > 1024 || c->pages < 0 ||
-        c->pages > INT32_MAX)
+        c->pages > INT32_MAX / (static_cast<int64_t>(c->kv_heads) * c->page))
         return SS24_ERR_SHAPE;
     if (c->pages > 0 && (!c->k || !c->v || !c->k_scales || !c->v_scales))
         return SS24_ERR_NULL;
@@ -91,7 +91,7 @@ bool plan_attention(const KvCache &c, const KvBatch &b, int32_t q_heads, KvAtten
     p->group = q_heads / c.kv_heads;
     kv_attend_plan(p);
     const double ctas = static_cast<double>(b.seqs) * c.kv_heads * p->row_tiles * p->splits;
-    return ctas < 2147483647.0 && static_cast<double>(b.tokens) * q_heads < 8.0 * 2147483647.0;
+    return ctas < 2147483647.0 && static_cast<double>(b.tokens) * q_heads < 2147483647.0;
 }
 
 int64_t scratch_floats(const KvAttendParams &p)
@@ -154,7 +154,7 @@ ss24_status ss24_kv_append(const ss24_kv_cache *cache, const ss24_kv_batch *batc
         return st;
     // the new tokens may start on a page's last slot
     p.page_slots = (p.batch.max_new + p.cache.page - 2) / p.cache.page + 1;
-    if (static_cast<double>(p.batch.seqs) * p.page_slots * 2 * p.cache.kv_heads >= 2147483647.0)
+    if (static_cast<double>(p.batch.seqs) * p.page_slots >= 2147483647.0)
         return SS24_ERR_SHAPE;
     p.err = error_word(ws);
     return cuda_status(launch_kv_append(p, k->dtype == SS24_F32, reinterpret_cast<cudaStream_t>(stream)));

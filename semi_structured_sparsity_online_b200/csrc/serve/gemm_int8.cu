@@ -387,27 +387,6 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
 }
 
-bool encode_rows(CUtensorMap *map, const int8_t *base, int64_t rows, int64_t k, uint32_t box_rows)
-{
-    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            fn = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }();
-    if (!encode)
-        return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-    cuuint64_t stride[1] = {static_cast<cuuint64_t>(k)};
-    cuuint32_t box[2] = {kBK, box_rows};
-    cuuint32_t one[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, stride, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename K, typename... A>
 cudaError_t launch_gemm(K kern, size_t smem, int64_t grid, int threads, int cluster, cudaStream_t stream, A... args)
 {
@@ -440,7 +419,7 @@ constexpr int64_t kSms = 148;
 template <int BN> cudaError_t launch_split(const GemmInt8Params &p, cudaStream_t stream)
 {
     CUtensorMap mw, mx;
-    if (!encode_rows(&mw, p.b, p.n, p.k, kBM) || !encode_rows(&mx, p.a, p.m, p.k, BN))
+    if (!tensor_map_bytes(&mw, p.b, p.n, p.k, kBK, kBM) || !tensor_map_bytes(&mx, p.a, p.m, p.k, kBK, BN))
         return cudaErrorInvalidValue;
     const int64_t tiles = ceil_div(p.n, kBM) * ceil_div(p.m, BN), nk = ceil_div(p.k, kBK);
     if (tiles > INT32_MAX / 8)
@@ -458,7 +437,7 @@ template <int BN> cudaError_t launch_split(const GemmInt8Params &p, cudaStream_t
 cudaError_t launch_pair(const GemmInt8Params &p, cudaStream_t stream)
 {
     CUtensorMap mw, mx;
-    if (!encode_rows(&mw, p.b, p.n, p.k, kBM) || !encode_rows(&mx, p.a, p.m, p.k, kBM))
+    if (!tensor_map_bytes(&mw, p.b, p.n, p.k, kBK, kBM) || !tensor_map_bytes(&mx, p.a, p.m, p.k, kBK, kBM))
         return cudaErrorInvalidValue;
     const int64_t tiles = ceil_div(p.n, 2 * kBM) * ceil_div(p.m, kPairN);
     const int64_t pairs = tiles < kSms / 2 ? tiles : kSms / 2;

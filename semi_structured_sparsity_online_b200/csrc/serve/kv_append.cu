@@ -18,15 +18,26 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 
-template <bool F32> __device__ __forceinline__ void load8(const void *base, int64_t at, float (&v)[8])
+// 8 elements as they lie in memory
+template <bool F32> struct Raw8 {
+    uint4 w[F32 ? 2 : 1];
+};
+template <bool F32> __device__ __forceinline__ void load8(const void *base, int64_t at, Raw8<F32> &r)
+{
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + at * (F32 ? 4 : 2));
+    r.w[0] = __ldg(x);
+    if constexpr (F32)
+        r.w[1] = __ldg(x + 1);
+}
+template <bool F32> __device__ __forceinline__ void values8(const Raw8<F32> &r, float (&v)[8])
 {
     if constexpr (F32) {
-        const float4 *x = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
-        const float4 a = __ldg(x), b = __ldg(x + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        const uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = __uint_as_float(u[i]);
     } else {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + at));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(u[i] << 16);
@@ -76,59 +87,57 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppen
 {
     __shared__ float warp_max[kAppendThreads / 32];
     const KvCache &c = p.cache;
-    int64_t b = blockIdx.x;
-    const int h = static_cast<int>(b % c.kv_heads);
-    b /= c.kv_heads;
-    const int kv = static_cast<int>(b & 1);
-    b >>= 1;
-    const int64_t slot = b % p.page_slots, s = b / p.page_slots;
+    const int h = blockIdx.y, kv = blockIdx.z;
+    const uint32_t s = blockIdx.x / static_cast<uint32_t>(p.page_slots), slot = blockIdx.x - s * p.page_slots;
+    grid_dependents_launch();
     grid_dependency_wait();
 
     int32_t first, count, len;
     if (!kv_sequence(p.batch, s, p.err, &first, &count, &len) || count == 0)
         return;
     const int32_t begin = len - count; // negative: the first tokens have no place
-    const int64_t pi = ((begin > 0 ? begin : 0) >> c.log2_page) + slot;
-    const int64_t p0 = pi << c.log2_page;
+    const int32_t pi = ((begin > 0 ? begin : 0) >> c.log2_page) + static_cast<int32_t>(slot);
+    const int64_t p0 = static_cast<int64_t>(pi) << c.log2_page;
     const int64_t lo = begin > p0 ? begin : p0, hi = len < p0 + c.page ? len : p0 + c.page;
     if (lo >= hi)
         return;
-    const int32_t id = p.batch.table[s * p.batch.table_ld + pi];
+    const int32_t id = __ldg(p.batch.table + s * p.batch.table_ld + pi);
+    const int fill = static_cast<int>(lo - p0), end = static_cast<int>(hi - p0); // new slots [fill, end)
+    const HeadRows &x = p.x[kv];
+    const int64_t row0 = first + (p0 - begin); // the token at slot 0
+    const int lg_cpr = c.d == 128 ? 4 : 3;     // chunks per token
+
+    // the tokens are on their way before the page number is looked at
+    Raw8<F32> raw[CPT];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        const int ch = threadIdx.x + i * kAppendThreads, t = ch >> lg_cpr;
+        if (t >= fill && t < end)
+            load8<F32>(x.x, (row0 + t) * x.token_ld + h * x.head_ld + 8 * (ch & ((1 << lg_cpr) - 1)), raw[i]);
+        else
+            raw[i] = Raw8<F32>{};
+    }
     if (id < 0 || id >= c.pages) {
         if (threadIdx.x == 0)
             atomicCAS(p.err, 0, kErrPage);
         return;
     }
-    const int fill = static_cast<int>(lo - p0), end = static_cast<int>(hi - p0); // new slots [fill, end)
     const int64_t page_head = static_cast<int64_t>(id) * c.kv_heads + h;
     uint8_t *codes = c.codes[kv] + (page_head << c.log2_page) * c.d;
-    const HeadRows &x = p.x[kv];
-    const int64_t row0 = first + (p0 - begin); // the token at slot 0
-    const int cpr = c.d >> 3;                  // chunks per token
-
-    float v[CPT][8];
+    const float had = fill > 0 ? c.scales[kv][page_head] : 0.0f;
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-        const int ch = threadIdx.x + i * kAppendThreads;
-        const int t = ch / cpr;
-        if (t >= fill && t < end)
-            load8<F32>(x.x, (row0 + t) * x.token_ld + h * x.head_ld + 8 * (ch % cpr), v[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i][j] = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < CPT; ++i)
+        float v[8];
+        values8<F32>(raw[i], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            amax = fmaxf(amax, fabsf(v[i][j]));
+            amax = fmaxf(amax, fabsf(v[j]));
+    }
     for (int o = 16; o; o >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     if ((threadIdx.x & 31) == 0)
         warp_max[threadIdx.x >> 5] = amax;
-    const float had = fill > 0 ? c.scales[kv][page_head] : 0.0f;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kAppendThreads / 32; ++w)
@@ -140,14 +149,15 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppen
     const bool grew = fill > 0 && s_new > had;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-        const int ch = threadIdx.x + i * kAppendThreads;
-        const int t = ch / cpr;
+        const int ch = threadIdx.x + i * kAppendThreads, t = ch >> lg_cpr;
         uint2 *at = reinterpret_cast<uint2 *>(codes) + ch;
+        float v[8];
         if (t >= fill && t < end) {
-            *at = encode8<FP8>(v[i], r);
+            values8<F32>(raw[i], v);
+            *at = encode8<FP8>(v, r);
         } else if (grew && t < fill) {
-            decode8<FP8>(*at, had, v[i]);
-            *at = encode8<FP8>(v[i], r);
+            decode8<FP8>(*at, had, v);
+            *at = encode8<FP8>(v, r);
         }
     }
 }
@@ -171,7 +181,7 @@ cudaError_t launch_kv_append(const KvAppendParams &p, int x_f32, cudaStream_t st
     const void *k = p.cache.fp8 ? (x_f32 ? append_kernel<true, true>(cpt) : append_kernel<true, false>(cpt))
                                 : (x_f32 ? append_kernel<false, true>(cpt) : append_kernel<false, false>(cpt));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.batch.seqs * p.page_slots * 2 * p.cache.kv_heads));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch.seqs * p.page_slots), static_cast<unsigned>(p.cache.kv_heads), 2);
     cfg.blockDim = dim3(kAppendThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -8,10 +8,11 @@
 // new tokens are rows of one tile: row r is token r / group, head r % group.
 // Both products run on the tensor cores with the keys (or the head dimension)
 // as the MMA's M and 8 rows as its N, so that 4 or 8 rows leave nothing idle.
-// The codes go from global memory to registers in 16-byte loads; the MMA's k
-// order is free as long as both operands agree, so no shuffle or shared
-// memory lies between a load and its MMA. Codes are exact in fp16 (|code| <=
-// 127, or E4M3). q is held in fp16 after a power-of-two scaling of its row by
+// Each warp walks over its own 16-key groups through its own ring of TMA boxes
+// (swizzled, so that the fragment reads hit distinct banks) and waits for no
+// other warp until its end; the MMA's k order is free as long as both operands
+// agree, so a fragment is 16 bytes of a key as they lie.
+// Codes are exact in fp16 (|code| <= 127, or E4M3). q is held in fp16 after a power-of-two scaling of its row by
 // its largest magnitude: what that drops is below 2^-24 of that magnitude.
 //
 // The weights of the second product carry the V scale: w = 2^(x + log2 s_v -
@@ -20,6 +21,7 @@
 // sum they enter. M moves only when a value exceeds it by 2^8. The denominator
 // sums w / s_v in binary32. Scales s_v below 2^-100 count as 2^-100.
 #include "kv_attend.cuh"
+#include "tcgen05.cuh"
 
 namespace ss24 {
 
@@ -48,72 +50,92 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
     return r;
 }
 
-__device__ __forceinline__ uint4 load_codes16(const uint8_t *p)
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
     return v;
 }
 
-// A warp's 16 keys. Lane (g, q) = (lane / 4, lane % 4) holds, of K, keys g and
-// g + 8: for D = 128 the 16 bytes at 64 c + 16 q, c = 0, 1 (D = 64: at 16 q);
-// of V, the D / 8 bytes at g D / 8 of keys 2q, 2q + 1, 2q + 8, 2q + 9.
-template <int D> struct Keys16 {
-    uint4 k[2][D / 64];
-    uint32_t v[4][D / 32];
-    float ks, vs;
-    bool there;
+constexpr int kRowWarps = 8;               // they take a part's 16-key groups in turn
+
+template <int D, int NT> struct RowShape {
+    static constexpr int kRing = (D == 128 ? 3 : 6) * (NT == 1 ? 1 : 2);
+    static constexpr uint32_t kBox = 16 * D;      // 16 keys of K or of V
+    static constexpr uint32_t kGroup = 2 * kBox;
+    static constexpr int kPerSm = NT == 1 ? 2 : 1;
+    // afterwards the boxes hold the warps' sums [warp][row][D + 4]
+    static constexpr uint32_t kSums = kRowWarps * 8 * NT * (D + 4) * 4;
+    static constexpr uint32_t kTiles =
+        kRowWarps * kRing * kGroup > kSums ? kRowWarps * kRing * kGroup : kSums;
+    static constexpr size_t kSmem = 1024 + kTiles + 2 * kRowWarps * 8 * NT * 4 + kRowWarps * kRing * 8;
 };
 
-template <int D>
-__device__ __forceinline__ void load_keys(Keys16<D> &t, const KvAttendParams &p, int32_t id, int h, int32_t key0,
-                                          int lane)
+// 16-byte chunk c of row r in a swizzled box.
+template <int D> __device__ __forceinline__ uint32_t box_chunk(int r, int c)
 {
-    t.there = id >= 0 && id < p.cache.pages;
-    if (!t.there)
-        return;
-    const int g = lane >> 2, q = lane & 3;
-    const int64_t ph = static_cast<int64_t>(id) * p.cache.kv_heads + h;
-    const int64_t at = ((ph << p.cache.log2_page) + (key0 & (p.cache.page - 1))) * D;
-    const uint8_t *k = p.cache.codes[0] + at + g * D + 16 * q, *v = p.cache.codes[1] + at + 2 * q * D + g * (D / 8);
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-        t.k[0][c] = load_codes16(k + 64 * c);
-        t.k[1][c] = load_codes16(k + 8 * D + 64 * c);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint8_t *at_i = v + ((i & 1) + 8 * (i >> 1)) * D;
-        if constexpr (D == 128) {
-            const uint4 w = load_codes16(at_i);
-            t.v[i][0] = w.x, t.v[i][1] = w.y, t.v[i][2] = w.z, t.v[i][3] = w.w;
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(at_i));
-            t.v[i][0] = w.x, t.v[i][1] = w.y;
-        }
-    }
-    t.ks = __ldg(p.cache.scales[0] + ph);
-    t.vs = __ldg(p.cache.scales[1] + ph);
+    return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// NT: n tiles of 8 rows; WARPS warps take turns on the part's 16-key steps.
-template <int D, bool FP8, int NT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) kv_attend_rows_kernel(const KvAttendParams p)
+// Sequences in order of falling length (equal ones by number), so that the CTAs
+// of a long one do not start last: on 64 sequences between 1024 and 8192 tokens
+// that leaves the SMs idle for a tenth of the call instead of a quarter. One
+// thread counts for one sequence; more of them than threads even out without.
+// `room`: shared memory for a number per thread.
+__device__ __forceinline__ int32_t longest_first(const KvBatch &b, uint32_t rank, int32_t *room)
 {
-    constexpr int ROWS = 8 * NT, MT = D / 16;
-    __shared__ float sm_o[WARPS][ROWS][D + 4];
-    __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
+    const int n = static_cast<int>(b.seqs), tid = threadIdx.x;
+    if (n == 1 || n > static_cast<int>(blockDim.x))
+        return rank;
+    const int32_t mine = tid < n ? __ldg(b.lengths + tid) : -1;
+    room[tid] = mine;
+    __syncthreads();
+    uint32_t before = 0;
+    if (tid < n)
+        for (int i = 0; i < n; ++i)
+            before += room[i] > mine || (room[i] == mine && i < tid);
+    __syncthreads();
+    if (tid < n && before == rank)
+        room[0] = tid;
+    __syncthreads();
+    const int32_t s = room[0];
+    __syncthreads();
+    return s;
+}
+
+// NT: n tiles of 8 rows.
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
+    kv_attend_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                          const KvAttendParams p)
+{
+    using S = RowShape<D, NT>;
+    constexpr int ROWS = 8 * NT, MT = D / 16, WARPS = kRowWarps, RING = S::kRing;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+    uint8_t *gen = smem_raw + (base - smem_u32(smem_raw));
+    float(*sm_o)[ROWS][D + 4] = reinterpret_cast<float(*)[ROWS][D + 4]>(gen);
+    float(*sm_m)[ROWS] = reinterpret_cast<float(*)[ROWS]>(gen + S::kTiles);
+    float(*sm_l)[ROWS] = sm_m + WARPS;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm_l + WARPS) + RING * (threadIdx.x >> 5); // this warp's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    int64_t b = blockIdx.x;
-    const int split = static_cast<int>(b % p.splits);
+    uint32_t b = blockIdx.x;
+    const int split = b % p.splits;
     b /= p.splits;
-    const int tile = static_cast<int>(b % p.row_tiles);
-    b /= p.row_tiles;
-    const int h = static_cast<int>(b % p.cache.kv_heads);
-    const int64_t s = b / p.cache.kv_heads;
+    const int h = b % p.cache.kv_heads;
+    b /= p.cache.kv_heads;
+    const int tile = b % p.row_tiles;
+    grid_dependents_launch();
     grid_dependency_wait();
+    const int64_t s = longest_first(p.batch, b / p.row_tiles, reinterpret_cast<int32_t *>(gen));
 
     int32_t first, count, len;
     const bool fine = kv_sequence(p.batch, s, p.err, &first, &count, &len);
@@ -127,6 +149,69 @@ __global__ void __launch_bounds__(WARPS * 32) kv_attend_rows_kernel(const KvAtte
     const int32_t last = row_at(p, row0 + live - 1, h, first, count, len).limit;
     if (ke > last)
         ke = last;
+
+    // this warp's groups: keys kb + 16 (warp + WARPS i)
+    const int all = ke > kb ? static_cast<int>((ke - kb + 15) / 16) : 0;
+    const int groups = all > warp ? (all - warp + WARPS - 1) / WARPS : 0;
+    if (lane == 0) {
+        for (int i = 0; i < RING; ++i)
+            mbar_init(&full[i], 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    bool failed = false;
+    const int32_t *table = p.batch.table + s * p.batch.table_ld;
+    const uint32_t ring = base + warp * (RING * S::kGroup);
+    auto key_of = [&](int i) { return static_cast<int32_t>(kb) + 16 * (warp + WARPS * i); };
+
+    // 32 groups at a time: lane i holds the page and scales of group 32 n + i;
+    // the next 32 pages are loaded meanwhile. -1: outside the cache, no keys.
+    auto load_id = [&](int i) {
+        if (i >= groups)
+            return -1;
+        return __ldg(table + (key_of(i) >> p.cache.log2_page));
+    };
+    int32_t id = load_id(lane), id_next = load_id(32 + lane);
+    float s_k, s_v, s_inv;
+    auto load_scales = [&] {
+        const bool on = id >= 0 && id < p.cache.pages;
+        const int64_t ph = on ? static_cast<int64_t>(id) * p.cache.kv_heads + h : 0;
+        s_k = on ? __ldg(p.cache.scales[0] + ph) : 0.0f;
+        const float v = on ? fmaxf(__ldg(p.cache.scales[1] + ph), 0x1p-100f) : 1.0f;
+        s_v = log2f(v);
+        s_inv = __frcp_rn(v);
+        if (!on)
+            id = -1;
+    };
+    // Copies of group i (of this warp), on page `page`, into a slot.
+    auto fetch = [&](int i, int slot, int32_t page) {
+        if (lane == 0) {
+            uint64_t *bar = &full[slot];
+            if (page < 0) {
+                mbar_arrive(bar);
+            } else {
+                const int32_t row =
+                    ((page * p.cache.kv_heads + h) << p.cache.log2_page) + (key_of(i) & (p.cache.page - 1));
+                const uint32_t at = ring + slot * S::kGroup;
+                mbar_arrive_expect_tx(bar, S::kGroup);
+                tc::tma_box(at, &map_k, 0, row, bar);
+                tc::tma_box(at + S::kBox, &map_v, 0, row, bar);
+            }
+        }
+    };
+    {
+        const bool bad = lane < groups && (id < 0 || id >= p.cache.pages);
+        if (bad)
+            atomicCAS(p.err, 0, kErrPage);
+        const int32_t page = bad || lane >= groups ? -1 : id;
+#pragma unroll
+        for (int i = 0; i < RING; ++i) {
+            const int32_t at = __shfl_sync(kFull, page, i);
+            if (i < groups)
+                fetch(i, i, at);
+        }
+    }
+    load_scales();
 
     // q: n tile t, row g: the 4 values of d that step ks of K's lane layout names
     uint32_t qf[NT][MT][2];
@@ -144,7 +229,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv_attend_rows_kernel(const KvAtte
 #pragma unroll
         for (int ks = 0; ks < MT; ++ks) {
             const uint2 w =
-                __ldg(reinterpret_cast<const uint2 *>(src + (ks / 4) * 64 + 16 * q + 4 * (ks & 3)));
+                __ldg(reinterpret_cast<const uint2 *>(src + (D / 4) * q + 4 * ks));
             v[ks][0] = on ? __uint_as_float(w.x << 16) : 0.0f;
             v[ks][1] = on ? __uint_as_float(w.x & 0xffff0000u) : 0.0f;
             v[ks][2] = on ? __uint_as_float(w.y << 16) : 0.0f;
@@ -181,106 +266,139 @@ __global__ void __launch_bounds__(WARPS * 32) kv_attend_rows_kernel(const KvAtte
     for (int t = 0; t < NT; ++t)
         m[t][0] = m[t][1] = -1e30f, l[t][0] = l[t][1] = 0.0f;
 
-    const int32_t *table = p.batch.table + s * p.batch.table_ld;
-    auto page_of = [&](int64_t key) { return key < ke ? __ldg(table + (key >> p.cache.log2_page)) : -1; };
-    int64_t key = kb + 16 * warp;
-    Keys16<D> next;
-    load_keys<D>(next, p, page_of(key), h, static_cast<int32_t>(key), lane);
-    int32_t id = page_of(key + 16 * WARPS);
-    for (; key < ke; key += 16 * WARPS) {
-        Keys16<D> cur = next;
-        load_keys<D>(next, p, id, h, static_cast<int32_t>(key + 16 * WARPS), lane);
-        id = page_of(key + 32 * WARPS);
-        if (!cur.there) {
-            if (lane == 0)
+    int slot = 0, phase = 0;
+    for (int i = 0; i < groups; ++i) {
+        if (i > 0 && (i & 31) == 0) {
+            id = id_next;
+            if (i + lane < groups && (id < 0 || id >= p.cache.pages))
                 atomicCAS(p.err, 0, kErrPage);
-            continue;
+            load_scales();
+            id_next = load_id(i + 32 + lane);
         }
-        float sc[NT][4] = {};
-#pragma unroll
-        for (int ks = 0; ks < MT; ++ks) {
-            const uint4 wa = cur.k[0][ks / 4], wb = cur.k[1][ks / 4];
-            const uint32_t a = (ks & 3) == 0 ? wa.x : (ks & 3) == 1 ? wa.y : (ks & 3) == 2 ? wa.z : wa.w;
-            const uint32_t c = (ks & 3) == 0 ? wb.x : (ks & 3) == 1 ? wb.y : (ks & 3) == 2 ? wb.z : wb.w;
-            uint32_t a0, a1, a2, a3;
-            codes4_to_f16<FP8>(a, a0, a2);
-            codes4_to_f16<FP8>(c, a1, a3);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                mma_f16(sc[t], a0, a1, a2, a3, qf[t][ks][0], qf[t][ks][1]);
+        const int32_t page = __shfl_sync(kFull, id, i & 31);
+        const float ks_i = __shfl_sync(kFull, s_k, i & 31), lsv = __shfl_sync(kFull, s_v, i & 31),
+                    inv = __shfl_sync(kFull, s_inv, i & 31);
+        if (!mbar_wait(&full[slot], phase, p.wait_limit_ns)) {
+            failed = true;
+            break;
         }
-        // sc[t]: (key g, rows 2q, 2q + 1), (key g + 8, the same rows)
-        const float sv = fmaxf(cur.vs, 0x1p-100f);
-        const float lsv = log2f(sv), inv = __frcp_rn(sv);
-        const bool edge = key + 16 > ke || key + 16 > low;
-        bool above = false;
+        const int32_t key = key_of(i);
+        const uint32_t k_at = ring + slot * S::kGroup, v_at = k_at + S::kBox;
+        if (page >= 0) {
+            // two chains of products, even and odd steps
+            float sc[NT][4] = {}, sd[NT][4] = {};
+            uint4 wa, wb;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sc[t][i] = fmaf(sc[t][i], cur.ks * fac[t][i & 1], lsv);
-                if (edge) {
-                    const int32_t j = static_cast<int32_t>(key) + g + 8 * (i >> 1);
-                    if (j >= limit[t][i & 1] || j >= ke)
-                        sc[t][i] = -INFINITY;
+            for (int ks = 0; ks < MT; ++ks) {
+                if ((ks & 3) == 0) {
+                    wa = lds16(k_at + box_chunk<D>(g, (D / 64) * q + ks / 4));
+                    wb = lds16(k_at + box_chunk<D>(g + 8, (D / 64) * q + ks / 4));
                 }
-                above |= sc[t][i] > m[t][i & 1] + 8.0f;
+                const uint32_t a = (ks & 3) == 0 ? wa.x : (ks & 3) == 1 ? wa.y : (ks & 3) == 2 ? wa.z : wa.w;
+                const uint32_t c = (ks & 3) == 0 ? wb.x : (ks & 3) == 1 ? wb.y : (ks & 3) == 2 ? wb.z : wb.w;
+                uint32_t a0, a1, a2, a3;
+                codes4_to_f16<FP8>(a, a0, a2);
+                codes4_to_f16<FP8>(c, a1, a3);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    mma_f16((ks & 1) ? sd[t] : sc[t], a0, a1, a2, a3, qf[t][ks][0], qf[t][ks][1]);
             }
-        if (__any_sync(kFull, above)) {
+            // sc[t]: (key g, rows 2q, 2q + 1), (key g + 8, the same rows)
+            const bool edge = key + 16 > ke || key + 16 > low;
+            bool above = false;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x = fmaxf(sc[t][i], sc[t][i + 2]);
-                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-                    x = fmaxf(x, m[t][i]);
-                    const float f = exp2_approx(m[t][i] - x);
-                    m[t][i] = x;
-                    l[t][i] *= f;
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        o[t][mt][i] *= f;
-                        o[t][mt][i + 2] *= f;
+                for (int i = 0; i < 4; ++i) {
+                    sc[t][i] = fmaf(sc[t][i] + sd[t][i], ks_i * fac[t][i & 1], lsv);
+                    if (edge) {
+                        const int32_t j = key + g + 8 * (i >> 1);
+                        if (j >= limit[t][i & 1] || j >= ke)
+                            sc[t][i] = -INFINITY;
                     }
+                    above |= sc[t][i] > m[t][i & 1] + 8.0f;
                 }
-        }
-        uint32_t pf[NT][2];
+            if (__any_sync(kFull, above)) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float w[4];
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = exp2_approx(sc[t][i] - m[t][i & 1]);
-            l[t][0] = fmaf(w[0] + w[2], inv, l[t][0]);
-            l[t][1] = fmaf(w[1] + w[3], inv, l[t][1]);
-            pf[t][0] = transpose8x8(pack_f16(w[0], w[1]));
-            pf[t][1] = transpose8x8(pack_f16(w[2], w[3]));
-        }
-        if (FP8 && key + 16 > ke) {
-            // slots behind the last token may hold NaN codes
+                    for (int i = 0; i < 2; ++i) {
+                        float x = fmaxf(sc[t][i], sc[t][i + 2]);
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+                        x = fmaxf(x, m[t][i]);
+                        const float f = exp2_approx(m[t][i] - x);
+                        m[t][i] = x;
+                        l[t][i] *= f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (key + 2 * q + (i & 1) + 8 * (i >> 1) >= ke)
-#pragma unroll
-                    for (int w = 0; w < D / 32; ++w)
-                        cur.v[i][w] = 0;
-        }
-        // m tile mt: rows g, g + 8 are elements g D / 8 + 2 mt, + 1
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            uint32_t lo[4], hi[4];
-            pairs4_to_f16<FP8>(cur.v[0][w], cur.v[1][w], lo);
-            pairs4_to_f16<FP8>(cur.v[2][w], cur.v[3][w], hi);
+                        for (int mt = 0; mt < MT; ++mt) {
+                            o[t][mt][i] *= f;
+                            o[t][mt][i + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t pf[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                mma_f16(o[t][2 * w], lo[0], lo[1], hi[0], hi[1], pf[t][0], pf[t][1]);
-                mma_f16(o[t][2 * w + 1], lo[2], lo[3], hi[2], hi[3], pf[t][0], pf[t][1]);
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = exp2_approx(sc[t][i] - m[t][i & 1]);
+                l[t][0] = fmaf(w[0] + w[2], inv, l[t][0]);
+                l[t][1] = fmaf(w[1] + w[3], inv, l[t][1]);
+                pf[t][0] = transpose8x8(pack_f16(w[0], w[1]));
+                pf[t][1] = transpose8x8(pack_f16(w[2], w[3]));
+            }
+            // of V, lane (g, q) takes the D / 8 bytes at g D / 8 of keys 2q, 2q + 1, 2q + 8, 2q + 9
+            uint32_t v[4][D / 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 2 * q + (i & 1) + 8 * (i >> 1);
+                if constexpr (D == 128) {
+                    const uint4 w = lds16(v_at + box_chunk<D>(r, g));
+                    v[i][0] = w.x, v[i][1] = w.y, v[i][2] = w.z, v[i][3] = w.w;
+                } else {
+                    const uint2 w = lds8(v_at + box_chunk<D>(r, g >> 1) + 8 * (g & 1));
+                    v[i][0] = w.x, v[i][1] = w.y;
+                }
+            }
+            if (FP8 && key + 16 > ke) {
+                // slots behind the last token may hold NaN codes
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (key + 2 * q + (i & 1) + 8 * (i >> 1) >= ke)
+#pragma unroll
+                        for (int w = 0; w < D / 32; ++w)
+                            v[i][w] = 0;
+            }
+            // m tile mt: rows g, g + 8 are elements g D / 8 + 2 mt, + 1
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                uint32_t lo[4], hi[4];
+                pairs4_to_f16<FP8>(v[0][w], v[1][w], lo);
+                pairs4_to_f16<FP8>(v[2][w], v[3][w], hi);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma_f16(o[t][2 * w], lo[0], lo[1], hi[0], hi[1], pf[t][0], pf[t][1]);
+                    mma_f16(o[t][2 * w + 1], lo[2], lo[3], hi[2], hi[3], pf[t][0], pf[t][1]);
+                }
             }
         }
+        // every lane has read the slot: the group RING on takes it
+        const int n = i + RING;
+        const int32_t page_n = __shfl_sync(kFull, (n ^ i) & ~31 ? id_next : id, n & 31);
+        if (n < groups)
+            fetch(n, slot, page_n < p.cache.pages ? page_n : -1);
+        if (++slot == RING)
+            slot = 0, phase ^= 1;
     }
-
+    // a wait that ran out: the copies on their way land before the CTA exits
+    if (failed)
+        for (int i = 0; i < RING; ++i)
+            (void)mbar_wait(&full[i], 0, p.wait_limit_ns / 8);
+    // every warp is through with the boxes before they take the sums
+    __syncthreads();
     // the warps' sums joined
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -297,6 +415,8 @@ __global__ void __launch_bounds__(WARPS * 32) kv_attend_rows_kernel(const KvAtte
                 *reinterpret_cast<float2 *>(&sm_o[warp][r][g * (D / 8) + 2 * mt]) =
                     make_float2(o[t][mt][i], o[t][mt][i + 2]);
         }
+    if (failed)
+        atomicCAS(p.err, 0, kErrAttendWait);
     __syncthreads();
     for (int e = threadIdx.x; e < live * (D / 4); e += WARPS * 32) {
         const int r = e / (D / 4), d = 4 * (e % (D / 4));
@@ -336,64 +456,102 @@ __global__ void __launch_bounds__(WARPS * 32) kv_attend_rows_kernel(const KvAtte
     }
 }
 
-// Joins the parts of the key axis: one warp per (token, query head).
-template <int D> __global__ void __launch_bounds__(256) kv_attend_join_kernel(const KvAttendParams p)
+// Joins the parts of the key axis: one CTA per (token, query head). Weights of
+// the parts first, then the warps sum every kJoinWarps-th part each, several
+// loads in flight.
+constexpr int kJoinWarps = 4, kMaxParts = 1024;
+
+template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) kv_attend_join_kernel(const KvAttendParams p)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t heads = static_cast<int64_t>(p.cache.kv_heads) * p.group;
-    const int64_t flat = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    __shared__ float weight[kMaxParts];
+    __shared__ float part_top[kJoinWarps], part_den[kJoinWarps];
+    __shared__ float sums[kJoinWarps][D];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = kJoinWarps * 32;
+    const int32_t heads = p.cache.kv_heads * p.group;
+    const int64_t flat = blockIdx.x;
+    const int32_t token = blockIdx.x / heads, head = blockIdx.x - token * heads;
     grid_dependency_wait();
     // tokens outside starts[0] .. starts[seqs] belong to no sequence
-    const int64_t token = flat / heads;
-    if (token >= p.batch.tokens || token < p.batch.starts[0] || token >= p.batch.starts[p.batch.seqs])
+    if (token < p.batch.starts[0] || token >= p.batch.starts[p.batch.seqs])
         return;
     const float *lse = p.part_lse + flat * p.splits;
     float top = -INFINITY;
-    for (int i = lane; i < p.splits; i += 32)
-        top = fmaxf(top, lse[i]);
+    for (int i = tid; i < p.splits; i += threads) {
+        const float x = lse[i];
+        weight[i] = x;
+        top = fmaxf(top, x);
+    }
     for (int o = 16; o; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    float acc[D / 32] = {};
-    float den = 0.0f;
-    if (top > -INFINITY) {
-        for (int i = 0; i < p.splits; ++i) {
-            const float w = exp2_approx(lse[i] - top);
-            if (w == 0.0f)
-                continue;
-            den += w;
-            const float *src = p.part_o + (flat * p.splits + i) * D + lane * (D / 32);
+    if (lane == 0)
+        part_top[warp] = top;
+    __syncthreads();
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j)
-                acc[j] = fmaf(w, src[j], acc[j]);
-        }
+    for (int w = 0; w < kJoinWarps; ++w)
+        top = fmaxf(top, part_top[w]);
+    const bool any = top > -INFINITY;
+    constexpr int PER = D / 32;
+    float acc[PER] = {};
+    float den = 0.0f;
+    const float *src = p.part_o + flat * p.splits * D + lane * PER;
+#pragma unroll 4
+    for (int i = warp; i < p.splits; i += kJoinWarps) {
+        // a part without keys for the row has weight 0 and finite sums (zeros)
+        const float w = any ? exp2_approx(weight[i] - top) : 0.0f;
+        float x[PER];
+        if constexpr (PER == 4)
+            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(src + static_cast<int64_t>(i) * D);
+        else
+            *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(src + static_cast<int64_t>(i) * D);
+        den += w;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            acc[j] = fmaf(w, x[j], acc[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        sums[warp][lane * PER + j] = acc[j];
+    if (lane == 0)
+        part_den[warp] = den;
+    __syncthreads();
+    if (tid >= D / 2)
+        return;
+    float2 r = make_float2(0.0f, 0.0f);
+    den = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        r.x += sums[w][2 * tid], r.y += sums[w][2 * tid + 1];
+        den += part_den[w];
     }
     const float inv = den > 0.0f ? __frcp_rn(den) : 0.0f;
-    const int64_t head = flat % heads;
     __nv_bfloat16 *dst =
-        static_cast<__nv_bfloat16 *>(p.out.x) + token * p.out.token_ld + head * p.out.head_ld + lane * (D / 32);
-#pragma unroll
-    for (int j = 0; j < D / 32; j += 2)
-        *reinterpret_cast<__nv_bfloat162 *>(dst + j) = __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
-    if (p.lse && lane == 0)
+        static_cast<__nv_bfloat16 *>(p.out.x) + token * p.out.token_ld + head * p.out.head_ld + 2 * tid;
+    *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(r.x * inv, r.y * inv);
+    if (p.lse && tid == 0)
         p.lse[flat] = den > 0.0f ? kLn2 * (top + log2f(den)) : -INFINITY;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-cudaError_t launch(const void *k, int64_t grid, int threads, const KvAttendParams &p, cudaStream_t stream)
+template <typename K, typename... A>
+cudaError_t launch(K kern, int64_t grid, int threads, size_t smem, cudaStream_t stream, A... args)
 {
+    if (smem > 0) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess)
+            return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    KvAttendParams pp = p;
-    void *args[1] = {&pp};
-    return cudaLaunchKernelExC(&cfg, k, args);
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Up to 16 rows per (sequence, KV head) go to the kernel above, in tiles of 8
@@ -401,10 +559,22 @@ cudaError_t launch(const void *k, int64_t grid, int threads, const KvAttendParam
 bool narrow(const KvAttendParams &p) { return p.batch.max_new * p.group <= 8; }
 bool wide(const KvAttendParams &p) { return p.batch.max_new * p.group > 16; }
 
-template <int D, bool FP8> const void *rows_kernel(bool one)
+template <int D, bool FP8, int NT> cudaError_t launch_rows(const KvAttendParams &p, cudaStream_t stream)
 {
-    return one ? reinterpret_cast<const void *>(kv_attend_rows_kernel<D, FP8, 1, 8>)
-               : reinterpret_cast<const void *>(kv_attend_rows_kernel<D, FP8, 2, 4>);
+    CUtensorMap mk, mv;
+    // a cache without pages: maps that no copy uses
+    const bool none = p.cache.pages == 0;
+    const int64_t rows = none ? 16 : p.cache.pages * p.cache.kv_heads * p.cache.page;
+    if (!tensor_map_bytes(&mk, none ? p.q.x : p.cache.codes[0], rows, D, D, 16) ||
+        !tensor_map_bytes(&mv, none ? p.q.x : p.cache.codes[1], rows, D, D, 16))
+        return cudaErrorInvalidValue;
+    return launch(kv_attend_rows_kernel<D, FP8, NT>, p.batch.seqs * p.cache.kv_heads * p.row_tiles * p.splits,
+                  kRowWarps * 32, RowShape<D, NT>::kSmem, stream, mk, mv, p);
+}
+
+template <int D, bool FP8> cudaError_t launch_rows(const KvAttendParams &p, cudaStream_t stream)
+{
+    return narrow(p) ? launch_rows<D, FP8, 1>(p, stream) : launch_rows<D, FP8, 2>(p, stream);
 }
 
 } // namespace
@@ -416,12 +586,15 @@ void kv_attend_plan(KvAttendParams *p)
     const int64_t tile = wide(*p) ? kTileRows : narrow(*p) ? 8 : 16;
     p->row_tiles = static_cast<int32_t>(ceil_div(rows, tile));
     const int64_t ctas = p->batch.seqs * p->cache.kv_heads * p->row_tiles;
-    // parts of the key axis: enough CTAs to fill the SMs, each with a few steps
-    const int64_t step = narrow(*p) || wide(*p) ? 128 : 64;
-    int64_t splits = ctas > 0 ? 148 * (wide(*p) ? 1 : 4) / ctas : 1;
+    // Parts of the key axis: as many CTAs as run at once and no more, of 256 keys
+    // or more. A second wave costs its start and end (131072 keys, 8 heads, 8 rows
+    // each: 53 us in one wave of 296, 58 in two, 68 in four); more parts than 256
+    // keys give cost as much as they save (500 keys: 7.3 - 7.9 us either way).
+    const int64_t step = 128;
+    int64_t splits = ctas > 0 ? 148 * (wide(*p) ? 1 : 2) / ctas : 1;
     const int64_t most = ceil_div(len, 2 * step);
     splits = splits > most ? most : splits;
-    splits = splits < 1 ? 1 : splits;
+    splits = splits < 1 ? 1 : splits > kMaxParts ? kMaxParts : splits;
     p->split_keys = static_cast<int32_t>(ceil_div(ceil_div(len, splits), step) * step);
     p->splits = static_cast<int32_t>(ceil_div(len, p->split_keys));
 }
@@ -429,19 +602,17 @@ void kv_attend_plan(KvAttendParams *p)
 cudaError_t launch_kv_attend(const KvAttendParams &p, cudaStream_t stream)
 {
     cudaError_t e;
-    if (wide(p)) {
+    if (wide(p))
         e = launch_kv_attend_tiles(p, stream);
-    } else {
-        const bool one = narrow(p);
-        const void *k = p.cache.d == 128 ? (p.cache.fp8 ? rows_kernel<128, true>(one) : rows_kernel<128, false>(one))
-                                         : (p.cache.fp8 ? rows_kernel<64, true>(one) : rows_kernel<64, false>(one));
-        e = launch(k, p.batch.seqs * p.cache.kv_heads * p.row_tiles * p.splits, one ? 256 : 128, p, stream);
-    }
+    else if (p.cache.d == 128)
+        e = p.cache.fp8 ? launch_rows<128, true>(p, stream) : launch_rows<128, false>(p, stream);
+    else
+        e = p.cache.fp8 ? launch_rows<64, true>(p, stream) : launch_rows<64, false>(p, stream);
     if (e != cudaSuccess || p.splits <= 1)
         return e;
-    const void *join = p.cache.d == 128 ? reinterpret_cast<const void *>(kv_attend_join_kernel<128>)
-                                        : reinterpret_cast<const void *>(kv_attend_join_kernel<64>);
-    return launch(join, ceil_div(p.batch.tokens * p.cache.kv_heads * p.group, 8), 256, p, stream);
+    const int64_t grid = p.batch.tokens * p.cache.kv_heads * p.group;
+    return p.cache.d == 128 ? launch(kv_attend_join_kernel<128>, grid, kJoinWarps * 32, 0, stream, p)
+                            : launch(kv_attend_join_kernel<64>, grid, kJoinWarps * 32, 0, stream, p);
 }
 
 } // namespace ss24

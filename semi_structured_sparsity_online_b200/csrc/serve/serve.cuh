@@ -77,6 +77,11 @@ cudaError_t launch_kv_append(const KvAppendParams &p, int x_f32, cudaStream_t st
 void kv_attend_plan(KvAttendParams *p);
 cudaError_t launch_kv_attend(const KvAttendParams &p, cudaStream_t stream);
 
+// A map of the [rows][row_bytes] byte matrix at base for boxes of box_bytes (64
+// or 128, the swizzle's span too) x box_rows.
+bool tensor_map_bytes(CUtensorMap *map, const void *base, int64_t rows, int64_t row_bytes, uint32_t box_bytes,
+                      uint32_t box_rows);
+
 // New tokens of sequence s and its length, checked against the call's bounds;
 // false (and the error word) where they do not hold, which leaves the
 // sequence out.
