@@ -91,7 +91,7 @@ bool plan_attention(const KvCache &c, const KvBatch &b, int32_t q_heads, KvAtten
     p->group = q_heads / c.kv_heads;
     kv_attend_plan(p);
     const double ctas = static_cast<double>(b.seqs) * c.kv_heads * p->row_tiles * p->splits;
-    return ctas < 2147483647.0 && static_cast<double>(b.tokens) * q_heads < 2147483647.0;
+    return 2.0 * ctas < 2147483647.0 && static_cast<double>(b.tokens) * q_heads < 2147483647.0;
 }
 
 int64_t scratch_floats(const KvAttendParams &p)

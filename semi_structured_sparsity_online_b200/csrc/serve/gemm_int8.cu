@@ -88,7 +88,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     PairBars *bars = reinterpret_cast<PairBars *>(stages + kPairStages * kPairStage);
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(bars + 1);
     float *sa = reinterpret_cast<float *>(stages + kPairStages * kPairStage + 512); // [2][kPairN]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tc::uniform(tid >> 5), lane = tid & 31;
     const uint32_t rank = tc::cluster_rank();
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int64_t tt = (p.m + kPairN - 1) / kPairN, ct = (p.n + 2 * kBM - 1) / (2 * kBM), tiles = tt * ct;
@@ -125,7 +125,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int32_t row_w = static_cast<int32_t>(c * 2 * kBM + rank * kBM);
             const int32_t row_x = static_cast<int32_t>(t * kPairN + rank * kBM);
             for (int kt = 0; kt < nk; ++kt) {
-                if (!mbar_wait(&bars->empty[it], phase ^ 1, p.wait_limit_ns)) {
+                if (!tc::wait(&bars->empty[it], phase ^ 1, p.wait_limit_ns)) {
                     failed = true;
                     break;
                 }
@@ -142,20 +142,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         // the stages' last readers: a CTA leaves only after its copies have landed
         for (int64_t j = issued > kPairStages ? issued - kPairStages : 0; j < issued; ++j)
-            if (!mbar_wait(&bars->empty[j % kPairStages], (j / kPairStages) & 1, p.wait_limit_ns))
+            if (!tc::wait(&bars->empty[j % kPairStages], (j / kPairStages) & 1, p.wait_limit_ns))
                 failed = true;
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+        const bool lead = lane == 0;
         constexpr uint32_t kI = i8_idesc(256, kPairN);
         int it = 0, phase = 0, n = 0;
         for (int64_t i = pair; i < tiles && !failed; i += pairs, ++n) {
             const int a = n & 1;
-            if (!mbar_wait(&bars->acc_empty[a], ((n >> 1) & 1) ^ 1, p.wait_limit_ns)) {
+            if (!tc::wait<true>(&bars->acc_empty[a], ((n >> 1) & 1) ^ 1, p.wait_limit_ns)) {
                 failed = true;
                 break;
             }
             tc::fence_after();
             for (int kt = 0; kt < nk; ++kt) {
-                if (!mbar_wait(&bars->full[it], phase, p.wait_limit_ns)) {
+                if (!tc::wait<true>(&bars->full[it], phase, p.wait_limit_ns)) {
                     failed = true;
                     break;
                 }
@@ -164,12 +165,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kBK / 32; ++j)
                     tc::mma_i8_pair(tmem + a * kPairN, tc::desc_kmajor(at + 32 * j),
-                                    tc::desc_kmajor(at + kBM * kBK + 32 * j), kI, (kt | j) != 0);
-                tc::commit_pair(&bars->empty[it]);
+                                    tc::desc_kmajor(at + kBM * kBK + 32 * j), kI, (kt | j) != 0, lead);
+                tc::commit_pair(&bars->empty[it], lead);
                 if (++it == kPairStages)
                     it = 0, phase ^= 1;
             }
-            tc::commit_pair(&bars->acc_full[a]);
+            tc::commit_pair(&bars->acc_full[a], lead);
         }
     } else if (warp >= 4) {
         // warps 4-7 take the tile's first 128 tokens, warps 8-11 the others
@@ -186,7 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int64_t own = t0 + 32 * w + lane;
             s[32 * w + lane] = own < p.m ? __ldg(p.a_scale + own) : 0.0f;
             named_barrier_sync(1 + half, 128);
-            if (!mbar_wait(&bars->acc_full[a], (n >> 1) & 1, p.wait_limit_ns)) {
+            if (!tc::wait(&bars->acc_full[a], (n >> 1) & 1, p.wait_limit_ns)) {
                 failed = true;
                 break;
             }
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(accbar + 1);
     float *sa = reinterpret_cast<float *>(accbar + 2);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tc::uniform(tid >> 5), lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x % parts);
     const int64_t ct = (p.n + kBM - 1) / kBM, tile = blockIdx.x / parts;
     const int64_t c0 = tile % ct * kBM, t0 = tile / ct * BN;
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         int issued = 0;
         for (int kt = kt0; kt < kt1; ++kt, ++issued) {
             const int s = issued % STAGES;
-            if (issued >= STAGES && !mbar_wait(&empty[s], (issued / STAGES - 1) & 1, p.wait_limit_ns)) {
+            if (issued >= STAGES && !tc::wait(&empty[s], (issued / STAGES - 1) & 1, p.wait_limit_ns)) {
                 failed = true;
                 break;
             }
@@ -303,12 +304,13 @@ __global__ void __launch_bounds__(kSplitThreads)
         }
         if (failed) // the copies already issued land before the CTA can exit
             for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-                (void)mbar_wait(&full[i % STAGES], (i / STAGES) & 1, p.wait_limit_ns);
-    } else if (warp == 1 && lane == 0) {
+                (void)tc::wait(&full[i % STAGES], (i / STAGES) & 1, p.wait_limit_ns);
+    } else if (warp == 1) {
+        const bool lead = lane == 0;
         constexpr uint32_t kI = i8_idesc(128, BN);
         for (int i = 0; i < kt1 - kt0; ++i) {
             const int s = i % STAGES;
-            if (!mbar_wait(&full[s], (i / STAGES) & 1, p.wait_limit_ns)) {
+            if (!tc::wait(&full[s], (i / STAGES) & 1, p.wait_limit_ns)) {
                 failed = true;
                 break;
             }
@@ -316,10 +318,10 @@ __global__ void __launch_bounds__(kSplitThreads)
             const uint32_t at = smem_u32(stages + s * S::kStage);
 #pragma unroll
             for (int j = 0; j < kBK / 32; ++j)
-                tc::mma_i8(tmem, tc::desc_kmajor(at + 32 * j), tc::desc_kmajor(at + kBM * kBK + 32 * j), kI, (i | j) != 0);
-            tc::commit(&empty[s]);
+                tc::mma_i8(tmem, tc::desc_kmajor(at + 32 * j), tc::desc_kmajor(at + kBM * kBK + 32 * j), kI, (i | j) != 0, lead);
+            tc::commit(&empty[s], lead);
         }
-        tc::commit(accbar);
+        tc::commit(accbar, lead);
     }
     __syncwarp();
     const int cols = static_cast<int>(p.m - t0 < BN ? p.m - t0 : BN);
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     const bool on = c < p.n;
     const float sb = on ? p.b_scale[c] : 0.0f;
     __syncthreads();
-    if (!mbar_wait(accbar, 0, p.wait_limit_ns))
+    if (!tc::wait(accbar, 0, p.wait_limit_ns))
         failed = true;
     tc::fence_after();
     const uint32_t acc = tmem + (static_cast<uint32_t>(32 * warp) << 16);

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
         const int32_t page = __shfl_sync(kFull, id, i & 31);
         const float ks_i = __shfl_sync(kFull, s_k, i & 31), lsv = __shfl_sync(kFull, s_v, i & 31),
                     inv = __shfl_sync(kFull, s_inv, i & 31);
-        if (!mbar_wait(&full[slot], phase, p.wait_limit_ns)) {
+        if (!tc::wait(&full[slot], phase, p.wait_limit_ns)) {
             failed = true;
             break;
         }
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
     // a wait that ran out: the copies on their way land before the CTA exits
     if (failed)
         for (int i = 0; i < RING; ++i)
-            (void)mbar_wait(&full[i], 0, p.wait_limit_ns / 8);
+            (void)tc::wait(&full[i], 0, p.wait_limit_ns / 8);
     // every warp is through with the boxes before they take the sums
     __syncthreads();
     // the warps' sums joined
@@ -583,7 +583,8 @@ void kv_attend_plan(KvAttendParams *p)
 {
     const int64_t rows = p->batch.max_new * p->group;
     const int64_t len = p->batch.max_len > 0 ? p->batch.max_len : 1;
-    const int64_t tile = wide(*p) ? kTileRows : narrow(*p) ? 8 : 16;
+    const int pair = wide(*p) && kv_attend_pairs(*p) ? 2 : 1;
+    const int64_t tile = wide(*p) ? pair * kTileRows : narrow(*p) ? 8 : 16;
     p->row_tiles = static_cast<int32_t>(ceil_div(rows, tile));
     const int64_t ctas = p->batch.seqs * p->cache.kv_heads * p->row_tiles;
     // Parts of the key axis: as many CTAs as run at once and no more, of 256 keys
@@ -591,7 +592,7 @@ void kv_attend_plan(KvAttendParams *p)
     // each: 53 us in one wave of 296, 58 in two, 68 in four); more parts than 256
     // keys give cost as much as they save (500 keys: 7.3 - 7.9 us either way).
     const int64_t step = 128;
-    int64_t splits = ctas > 0 ? 148 * (wide(*p) ? 1 : 2) / ctas : 1;
+    int64_t splits = ctas > 0 ? 148 * (wide(*p) ? 1 : 2) / (pair * ctas) : 1;
     const int64_t most = ceil_div(len, 2 * step);
     splits = splits > most ? most : splits;
     splits = splits < 1 ? 1 : splits > kMaxParts ? kMaxParts : splits;

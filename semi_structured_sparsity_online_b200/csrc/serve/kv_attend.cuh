@@ -59,6 +59,12 @@ __device__ __forceinline__ RowAt row_at(const KvAttendParams &p, int64_t r, int 
 // Attention on the 5th-generation tensor cores, tiles of 128 or 256 rows
 // (kv_attend_tiles.cu).
 constexpr int kTileRows = 256;
+// Whether pairs of CTAs take 512 rows together: heads of 128 and more rows than
+// one CTA holds.
+inline bool kv_attend_pairs(const KvAttendParams &p)
+{
+    return p.cache.d == 128 && p.batch.max_new * p.group > kTileRows;
+}
 cudaError_t launch_kv_attend_tiles(const KvAttendParams &p, cudaStream_t stream);
 
 } // namespace ss24

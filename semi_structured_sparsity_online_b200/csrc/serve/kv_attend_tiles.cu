@@ -12,6 +12,14 @@
 //             P in tensor memory and V as it lies (MN-major)
 //   9-15      codes of K and V from the pages to fp16 in shared memory, a ring
 //             of stages in the 128-byte swizzle that the MMA reads
+// PAIR: two CTAs of a cluster work on twice the rows with cta_group::2 MMAs.
+// Each brings half of every B operand (64 keys of K, 64 of the 128 elements of
+// V) and its own rows: a step's shared-memory traffic per SM, which bounds the
+// single form (192 KB of MMA reads and 128 KB of conversion, 2500 cycles
+// against 2048 of MMA), halves on the side of the keys, and so does the
+// conversion. The even CTA's lane issues for both; barriers that it waits on
+// are arrived on by both.
+//
 // The two row tiles take turns: while one warpgroup works on its S, the
 // tensor cores serve the other. A new S overwrites the weights of the step
 // before; MMAs of one thread run in order, and the commit behind S(j + 1) also
@@ -29,23 +37,28 @@ constexpr int kTileThreads = 512;
 constexpr int kRegsRows = 176, kRegsRest = 80;
 constexpr int kKeys = 128;   // keys per step
 constexpr int kConvWarps = 7;
-constexpr int kRing = 4;     // fp16 stages: K and V of a step take one each
-constexpr int kRaw = 2;      // stages of codes on their way from the pages
-constexpr int kScaleRing = 4; // steps of page scales
 
-template <int D> struct TileShape {
-    static constexpr uint32_t kStage = kKeys * D * 2; // also a row tile of q
-    static constexpr uint32_t kAtom = kKeys * 128;    // 128 rows x 128 bytes
-    static constexpr uint32_t kCodes = kKeys * D;     // a stage's codes
-    static constexpr uint32_t kTiles = (2 + kRing) * kStage + kRaw * kCodes;
-    static constexpr size_t kSmem = 1024 + kTiles + kScaleRing * 8 * 16 + 256;
+template <int D, bool PAIR> struct TileShape {
+    static constexpr int kKRows = PAIR ? kKeys / 2 : kKeys; // keys of K in this CTA
+    static constexpr int kVCols = PAIR ? D / 2 : D;         // elements of V in this CTA
+    static constexpr int kRing = PAIR ? 8 : 4;              // fp16 stages: K and V of a step take one each
+    static constexpr int kRaw = PAIR ? 3 : 2;               // stages of codes on their way from the pages
+    static constexpr int kScaleRing = kRing / 2 + 2;        // steps of page scales
+    static constexpr uint32_t kQ = 128 * D * 2;             // a row tile of q
+    static constexpr uint32_t kStage = kKRows * D * 2;      // equals kKeys * kVCols * 2
+    static constexpr uint32_t kQAtom = 128 * 128, kKAtom = kKRows * 128, kVAtom = kKeys * 128; // 128-byte columns
+    static constexpr uint32_t kCodes = kKRows * D;          // a stage's codes
+    static constexpr uint32_t kTiles = 2 * kQ + kRing * kStage + kRaw * kCodes;
+    static constexpr size_t kSmem = 1024 + kTiles + kScaleRing * 8 * 16 + 512;
     static_assert(kSmem <= 232448, "shared memory per CTA");
+    static_assert(!PAIR || D == 128, "half of V's columns fill a swizzle row");
 };
 
 constexpr uint32_t kCols = 512; // S0 0, S1 128, O0 256, O1 384
-__host__ __device__ constexpr uint32_t f16_idesc(int n, bool b_mn)
+__host__ __device__ constexpr uint32_t f16_idesc(int m, int n, bool b_mn)
 {
-    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 template <int N> __device__ __forceinline__ void regs_up()
@@ -66,14 +79,15 @@ __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c)
     return r;
 }
 
+constexpr int kMaxRing = 8;
 struct Bars {
-    uint64_t kv_full[kRing], kv_empty[kRing], q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
+    uint64_t kv_full[kMaxRing], kv_empty[kMaxRing], q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
 };
 
-// 16-byte chunk c (8 fp16) of row r in a tile of D / 64 swizzled atoms.
-template <int D> __device__ __forceinline__ uint32_t chunk_at(int r, int c)
+// 16-byte chunk c (8 fp16) of row r in swizzled atoms of 128 bytes a row.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t atom, int r, int c)
 {
-    return (c >> 3) * TileShape<D>::kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    return (c >> 3) * atom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
@@ -81,23 +95,25 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool PAIR>
 __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const KvAttendParams p)
 {
-    using S = TileShape<D>;
+    using S = TileShape<D, PAIR>;
+    constexpr int RING = S::kRing, CTAS = PAIR ? 2 : 1, ROWS = CTAS * kTileRows;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     uint8_t *gen = smem_raw + (base - smem_u32(smem_raw));
-    const uint32_t sq = base, skv = base + 2 * S::kStage;
-    float4 *scales = reinterpret_cast<float4 *>(gen + S::kTiles); // [kScaleRing][8]: s_k, log2 s_v, 1 / s_v
-    Bars *bars = reinterpret_cast<Bars *>(scales + kScaleRing * 8);
+    const uint32_t sq = base, skv = base + 2 * S::kQ;
+    float4 *scales = reinterpret_cast<float4 *>(gen + S::kTiles); // [][8]: s_k, log2 s_v, 1 / s_v
+    Bars *bars = reinterpret_cast<Bars *>(scales + S::kScaleRing * 8);
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(bars + 1);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t b = blockIdx.x;
-    const int split = static_cast<int>(b % p.splits);
+    const int tid = threadIdx.x, warp = tc::uniform(tid >> 5), lane = tid & 31;
+    const uint32_t rank = PAIR ? tc::cluster_rank() : 0;
+    uint32_t b = blockIdx.x / CTAS;
+    const int split = b % p.splits;
     b /= p.splits;
-    const int h = static_cast<int>(b % p.cache.kv_heads);
+    const int h = b % p.cache.kv_heads;
     b /= p.cache.kv_heads;
     // the last row tiles see the most keys: they start first
     const int64_t tile = p.row_tiles - 1 - b % p.row_tiles, s = b / p.row_tiles;
@@ -105,44 +121,62 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
 
     int32_t first, count, len;
     const bool fine = kv_sequence(p.batch, s, p.err, &first, &count, &len);
-    const int64_t row0 = tile * kTileRows, rows = static_cast<int64_t>(count) * p.group;
+    const int64_t row0 = tile * ROWS, rows = static_cast<int64_t>(count) * p.group;
     if (!fine || row0 >= rows)
         return;
-    const int live = static_cast<int>(rows - row0 < kTileRows ? rows - row0 : kTileRows);
-    const bool two = live > 128;
+    // MMA row tile w holds rows 128 CTAS w on; the CTA of rank r its r-th 128
+    const int live = static_cast<int>(rows - row0 < ROWS ? rows - row0 : ROWS);
+    const bool two = tc::uniform(live > 128 * CTAS);
     const int64_t kb = static_cast<int64_t>(split) * p.split_keys;
     int64_t ke = kb + p.split_keys;
     const int32_t last = row_at(p, row0 + live - 1, h, first, count, len).limit;
     if (ke > last)
         ke = last;
-    const int steps = ke > kb ? static_cast<int>((ke - kb + kKeys - 1) / kKeys) : 0;
+    const int steps = tc::uniform(ke > kb ? static_cast<int>((ke - kb + kKeys - 1) / kKeys) : 0);
 
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(&bars->kv_full[i], 32 * kConvWarps);
+        // arrivals come from warps, of both CTAs
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&bars->kv_full[i], CTAS * kConvWarps);
             mbar_init(&bars->kv_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->q_full[i], 128);
+            mbar_init(&bars->q_full[i], CTAS * 4);
             mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_half[i], 128);
-            mbar_init(&bars->p_full[i], 128);
+            mbar_init(&bars->p_half[i], CTAS * 4);
+            mbar_init(&bars->p_full[i], CTAS * 4);
             mbar_init(&bars->o_full[i], 1);
         }
         fence_barrier_init();
     }
-    if (warp == 8)
-        tc::alloc(tmem_base, kCols);
+    if (warp == 8) {
+        if constexpr (PAIR)
+            tc::alloc_pair(tmem_base, kCols);
+        else
+            tc::alloc(tmem_base, kCols);
+    }
     tc::fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        tc::cluster_sync();
     tc::fence_after();
     const uint32_t tmem = *tmem_base;
     bool failed = false;
+    // a warp's arrival on a barrier that the issuing lane waits on
+    auto arrive = [&](uint64_t *bar) {
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (PAIR)
+                tc::arrive_cluster(tc::cluster_addr(smem_u32(bar), 0));
+            else
+                mbar_arrive(bar);
+        }
+    };
 
     if (warp < 8) {
         // ---- a row per thread -------------------------------------------------
         regs_up<kRegsRows>();
-        const int w = warp >> 2, r = tid & 127, row = 128 * w + r;
+        const int w = warp >> 2, r = tid & 127, row = 128 * (CTAS * w + rank) + r;
         if (w == 0 || two) {
             const bool on = row < live;
             const RowAt a = row_at(p, row0 + (on ? row : 0), h, first, count, len);
@@ -171,11 +205,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         f[i] = pack_f16(__uint_as_float(u[i] << 16) * down, __uint_as_float(u[i] & 0xffff0000u) * down);
-                    sts16(sq + w * S::kStage + chunk_at<D>(r, c), f[0], f[1], f[2], f[3]);
+                    sts16(sq + w * S::kQ + chunk_at(S::kQAtom, r, c), f[0], f[1], f[2], f[3]);
                 }
             }
             tc::fence_proxy();
-            mbar_arrive(&bars->q_full[w]);
+            arrive(&bars->q_full[w]);
 
             const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
             const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
@@ -184,14 +218,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             auto factor = [&](float s_k) { return fmaxf(s_k * fac, 0x1p-126f); };
             float m = -1e30f, l = 0.0f;
             for (int j = 0; j < steps; ++j) {
-                if (!mbar_wait(&bars->s_full[w], j & 1, p.wait_limit_ns)) {
+                if (!tc::wait(&bars->s_full[w], j & 1, p.wait_limit_ns)) {
                     failed = true;
                     break;
                 }
                 tc::fence_after();
                 const int32_t key0 = static_cast<int32_t>(kb) + j * kKeys;
                 const bool edge = key0 + kKeys > low;
-                const float4 *sc = scales + (j % kScaleRing) * 8;
+                const float4 *sc = scales + (j % S::kScaleRing) * 8;
                 uint32_t v[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -257,13 +291,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                         // half of the step's weights: its products may start
                         tc::wait_st();
                         tc::fence_before();
-                        mbar_arrive(c == 1 ? &bars->p_half[w] : &bars->p_full[w]);
+                        arrive(c == 1 ? &bars->p_half[w] : &bars->p_full[w]);
                     }
                 }
             }
 
             // ---- the row's output -------------------------------------------------
-            if (!failed && steps > 0 && !mbar_wait(&bars->o_full[w], 0, p.wait_limit_ns))
+            if (!failed && steps > 0 && !tc::wait(&bars->o_full[w], 0, p.wait_limit_ns))
                 failed = true;
             tc::fence_after();
             const bool any = steps > 0 && l > 0.0f;
@@ -315,14 +349,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
     } else if (warp > 8) {
         // ---- codes to fp16 ------------------------------------------------------
         regs_down<kRegsRest>();
-        constexpr int CPR = D / 16;            // 16-code chunks per key
-        constexpr int RPW = 32 / CPR;          // keys a warp takes at a time
-        constexpr int GROUPS = kKeys / RPW;    // D = 128: 32 groups of 4 keys; D = 64: 16 of 8
+        // Of K and of V: 16-code chunks per key in this CTA, keys a warp takes at a
+        // time, groups of those
+        constexpr int CPR[2] = {D / 16, S::kVCols / 16};
+        constexpr int RPW[2] = {32 / CPR[0], 32 / CPR[1]};
+        constexpr int GROUPS = S::kKRows / RPW[0]; // the same for V
         constexpr int ITERS = (GROUPS + kConvWarps - 1) / kConvWarps;
-        const int cw = warp - 9, kr = lane / CPR, cc = lane % CPR;
+        static_assert(kKeys / RPW[1] == GROUPS, "K and V items have one size");
+        const int cw = warp - 9;
+        const int kr[2] = {lane / CPR[0], lane / CPR[1]}, cc[2] = {lane % CPR[0], lane % CPR[1]};
         const int32_t *table = p.batch.table + s * p.batch.table_ld;
         const int items = 2 * steps;
-        const uint32_t raw = skv + kRing * S::kStage + 16 * lane;
+        const uint32_t raw = skv + RING * S::kStage + 16 * lane;
         // Group g of this warp's iteration; beyond the last group there is none.
         auto group = [&](int it) { return it * kConvWarps + cw; };
         auto page_at = [&](int32_t key) { return key < ke ? __ldg(table + (key >> p.cache.log2_page)) : -2; };
@@ -333,38 +371,34 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             }
             return id;
         };
+        // The key of this lane in iteration `it` of step j, K (0) or V (1).
+        auto key_at = [&](int j, int kv, int it) {
+            return static_cast<int32_t>(kb) + j * kKeys + (kv == 0 ? static_cast<int32_t>(rank) * S::kKRows : 0) +
+                   group(it) * RPW[kv] + kr[kv];
+        };
         // Codes travel by asynchronous copies, kRaw items ahead; a thread reads
         // back only what it copied itself. Keys past the end and pages outside
-        // the cache are zeros. A step's page numbers are loaded a step before
-        // they are used; its K and V share the offsets.
-        int64_t at[ITERS]; // byte offset of this thread's codes, -1: none
-        int32_t next_ids[ITERS];
-        auto load_ids = [&](int j) {
+        // the cache are zeros. Page numbers are loaded a step before they are used.
+        int32_t ids[2][ITERS];
+        auto load_ids = [&](int j, int kv) {
 #pragma unroll
             for (int it = 0; it < ITERS; ++it)
-                next_ids[it] = group(it) < GROUPS
-                                   ? page_at(static_cast<int32_t>(kb) + j * kKeys + group(it) * RPW + kr) : -2;
+                ids[kv][it] = group(it) < GROUPS ? page_at(key_at(j, kv, it)) : -2;
         };
-        auto fetch = [&](int item) {
+        auto fetch = [&](int item, int slot, int kv) { // kv = item & 1
             if (item < items) {
-                if ((item & 1) == 0) {
-                    const int32_t key0 = static_cast<int32_t>(kb) + (item >> 1) * kKeys + kr;
+                const uint8_t *codes = p.cache.codes[kv] + 16 * cc[kv] + (kv == 1 ? rank * S::kVCols : 0);
 #pragma unroll
-                    for (int it = 0; it < ITERS; ++it) {
-                        const int32_t id = checked(next_ids[it]);
-                        const int32_t slot = (key0 + group(it) * RPW) & (p.cache.page - 1);
-                        at[it] = id < 0 ? -1 : (((static_cast<int64_t>(id) * p.cache.kv_heads + h) << p.cache.log2_page) +
-                                                slot) * D + 16 * cc;
-                    }
-                    load_ids((item >> 1) + 1);
-                }
-                const uint8_t *codes = p.cache.codes[item & 1];
-#pragma unroll
-                for (int it = 0; it < ITERS; ++it)
+                for (int it = 0; it < ITERS; ++it) {
+                    const int32_t id = checked(ids[kv][it]);
+                    const int64_t at = ((static_cast<int64_t>(id) * p.cache.kv_heads + h) << p.cache.log2_page) +
+                                       (key_at(item >> 1, kv, it) & (p.cache.page - 1));
                     if (group(it) < GROUPS)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                         raw + (item % kRaw) * S::kCodes + group(it) * 512),
-                                     "l"(codes + (at[it] < 0 ? 0 : at[it])), "r"(at[it] < 0 ? 0 : 16));
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + slot * S::kCodes +
+                                                                                             group(it) * 512),
+                                     "l"(codes + (id < 0 ? 0 : at * D)), "r"(id < 0 ? 0 : 16));
+                }
+                load_ids((item >> 1) + 1, kv);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -383,123 +417,158 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             s_k = on ? __ldg(p.cache.scales[0] + ph) : 0.0f;
             s_v = on ? __ldg(p.cache.scales[1] + ph) : -1.0f;
         };
-        load_ids(0);
-        load_scale_id(0);
-        load_scales();
-        load_scale_id(1);
-        for (int item = 0; item < kRaw; ++item)
-            fetch(item);
-        for (int item = 0; item < items; ++item) {
-            const int st = item % kRing;
-            if (item >= kRing && !mbar_wait(&bars->kv_empty[st], (item / kRing - 1) & 1, p.wait_limit_ns)) {
-                failed = true;
-                break;
-            }
-            asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-            const uint32_t dst = skv + st * S::kStage;
+        // One item: the codes in a raw slot to fp16 in a stage.
+        auto convert = [&](int raw_slot, uint32_t dst, int kv) {
             uint32_t u[ITERS][4];
 #pragma unroll
             for (int it = 0; it < ITERS; ++it)
                 if (group(it) < GROUPS)
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(u[it][0]), "=r"(u[it][1]), "=r"(u[it][2]), "=r"(u[it][3])
-                                 : "r"(raw + (item % kRaw) * S::kCodes + group(it) * 512));
+                                 : "r"(raw + raw_slot * S::kCodes + group(it) * 512));
 #pragma unroll
             for (int it = 0; it < ITERS; ++it) {
                 uint32_t f[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     codes4_to_f16<FP8>(u[it][i], f[2 * i], f[2 * i + 1]);
-                // the second half of a row's lanes swaps its two stores: all 8 lanes of a
-                // store phase then hit different banks
-                const int r = group(it) * RPW + kr;
-                const bool odd = (cc & 4) != 0;
-                const uint32_t a0 = dst + chunk_at<D>(r, 2 * cc), a1 = a0 ^ 16;
+                // where 8 lanes write one row, the second four swap their two stores: all
+                // 8 lanes of a store phase then hit different banks
+                const bool odd = CPR[kv] == 8 && (cc[kv] & 4) != 0;
+                const uint32_t a0 = dst + chunk_at(kv == 0 ? S::kKAtom : S::kVAtom, group(it) * RPW[kv] + kr[kv], 2 * cc[kv]);
+                const uint32_t a1 = a0 ^ 16;
                 if (group(it) < GROUPS) {
                     sts16(odd ? a1 : a0, odd ? f[4] : f[0], odd ? f[5] : f[1], odd ? f[6] : f[2], odd ? f[7] : f[3]);
                     sts16(odd ? a0 : a1, odd ? f[0] : f[4], odd ? f[1] : f[5], odd ? f[2] : f[6], odd ? f[3] : f[7]);
                 }
             }
-            if ((item & 1) == 0 && scaler) {
-                // with a step's K, the scales of its 16-key groups
-                const float sv = fmaxf(s_v, 0x1p-100f);
-                scales[(item / 2 % kScaleRing) * 8 + lane] =
-                    s_v < 0.0f ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-                               : make_float4(s_k, log2f(sv), __frcp_rn(sv), 0.0f);
+        };
+        load_ids(0, 0);
+        load_ids(0, 1);
+        load_scale_id(0);
+        load_scales();
+        load_scale_id(1);
+#pragma unroll
+        for (int item = 0; item < S::kRaw; ++item)
+            fetch(item, item, item & 1);
+        int st = 0, phase = 1, raw_slot = 0;
+        for (int j = 0; j < steps && !failed; ++j) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                if (!tc::wait(&bars->kv_empty[st], phase, p.wait_limit_ns)) {
+                    failed = true;
+                    break;
+                }
+                asm volatile("cp.async.wait_group %0;" ::"n"(S::kRaw - 1) : "memory");
+                convert(raw_slot, skv + st * S::kStage, kv);
+                if (kv == 0 && scaler) {
+                    // with a step's K, the scales of its 16-key groups
+                    const float sv = fmaxf(s_v, 0x1p-100f);
+                    scales[(j % S::kScaleRing) * 8 + lane] =
+                        s_v < 0.0f ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+                                   : make_float4(s_k, log2f(sv), __frcp_rn(sv), 0.0f);
+                }
+                tc::fence_proxy();
+                arrive(&bars->kv_full[st]);
+                if (kv == 0 && scaler) {
+                    load_scales();
+                    load_scale_id(j + 2);
+                }
+                fetch(2 * j + kv + S::kRaw, raw_slot, (kv + S::kRaw) & 1);
+                if (++st == RING)
+                    st = 0, phase ^= 1;
+                if (++raw_slot == S::kRaw)
+                    raw_slot = 0;
             }
-            tc::fence_proxy();
-            mbar_arrive(&bars->kv_full[st]);
-            if ((item & 1) == 0 && scaler) {
-                load_scales();
-                load_scale_id((item >> 1) + 2);
-            }
-            fetch(item + kRaw);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         regs_down<kRegsRest>();
-        if (lane == 0 && steps > 0) {
-        // ---- MMAs -----------------------------------------------------------------
-        constexpr uint32_t kIS = f16_idesc(kKeys, false), kIO = f16_idesc(D, true);
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (!failed && !mbar_wait(bar, parity, p.wait_limit_ns))
-                failed = true;
-            return !failed;
-        };
-        auto scores = [&](int w, int st) {
-            const uint32_t q = sq + w * S::kStage, k = skv + st * S::kStage;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * S::kAtom + (ks & 3) * 32;
-                tc::mma_f16(tmem + 128 * w, tc::desc_kmajor(q + off), tc::desc_kmajor(k + off), kIS, ks > 0);
-            }
-            tc::commit(&bars->s_full[w]);
-        };
-        // the first or second half of a step's keys
-        auto values = [&](int w, int st, int j, int half) {
-            const uint32_t v = skv + st * S::kStage;
-#pragma unroll
-            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                tc::mma_f16_ta(tmem + 256 + 128 * w, tmem + 128 * w + 8 * ks, tc::desc_mnmajor(v + ks * 2048, S::kAtom), kIO,
-                               j > 0 || ks > 0);
-        };
-        const int tiles = two ? 2 : 1;
-        for (int w = 0; w < tiles; ++w)
-            wait(&bars->q_full[w], 0);
-        if (wait(&bars->kv_full[0], 0)) {
-            tc::fence_after();
-            for (int w = 0; w < tiles; ++w)
-                scores(w, 0);
-            tc::commit(&bars->kv_empty[0]);
-        }
-        for (int j = 0; j < steps && !failed; ++j) {
-            const int vi = 2 * j + 1, ki = 2 * j + 2, vs = vi % kRing, ks = ki % kRing;
-            wait(&bars->kv_full[vs], (vi / kRing) & 1);
-            for (int w = 0; w < tiles; ++w) {
-                if (!wait(&bars->p_half[w], j & 1))
-                    break;
+        if (warp == 8 && rank == 0 && steps > 0) {
+            const bool lead = lane == 0;
+            // ---- MMAs -----------------------------------------------------------
+            constexpr uint32_t kIS = f16_idesc(128 * CTAS, kKeys, false), kIO = f16_idesc(128 * CTAS, D, true);
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                const bool ok = tc::wait<PAIR>(bar, parity, p.wait_limit_ns);
                 tc::fence_after();
-                values(w, vs, j, 0);
-                if (!wait(&bars->p_full[w], j & 1))
-                    break;
-                tc::fence_after();
-                values(w, vs, j, 1);
-                if (w == tiles - 1)
-                    tc::commit(&bars->kv_empty[vs]);
-                if (j + 1 < steps) {
-                    if (w == 0 && !wait(&bars->kv_full[ks], (ki / kRing) & 1))
-                        break;
-                    tc::fence_after();
-                    scores(w, ks);
-                    if (w == tiles - 1)
-                        tc::commit(&bars->kv_empty[ks]);
+                failed = __any_sync(kFull, !ok);
+                return !failed;
+            };
+            auto commit = [&](uint64_t *bar) {
+                if constexpr (PAIR)
+                    tc::commit_pair(bar, lead);
+                else
+                    tc::commit(bar, lead);
+            };
+            auto scores = [&](int w, int st) {
+                const uint32_t q = sq + w * S::kQ, k = skv + st * S::kStage;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint64_t a = tc::desc_kmajor(q + (ks >> 2) * S::kQAtom + (ks & 3) * 32);
+                    const uint64_t b = tc::desc_kmajor(k + (ks >> 2) * S::kKAtom + (ks & 3) * 32);
+                    if constexpr (PAIR)
+                        tc::mma_f16_pair(tmem + 128 * w, a, b, kIS, ks > 0, lead);
+                    else
+                        tc::mma_f16(tmem + 128 * w, a, b, kIS, ks > 0, lead);
                 }
+                commit(&bars->s_full[w]);
+            };
+            // the first or second half of a step's keys
+            auto values = [&](int w, int st, int j, int half) {
+                const uint32_t v = skv + st * S::kStage;
+#pragma unroll
+                for (int ks = 4 * half; ks < 4 * half + 4; ++ks) {
+                    const uint64_t b = tc::desc_mnmajor(v + ks * 2048, S::kVAtom);
+                    const uint32_t a = tmem + 128 * w + 8 * ks, d = tmem + 256 + 128 * w;
+                    if constexpr (PAIR)
+                        tc::mma_f16_ta_pair(d, a, b, kIO, j > 0 || ks > 0, lead);
+                    else
+                        tc::mma_f16_ta(d, a, b, kIO, j > 0 || ks > 0, lead);
+                }
+            };
+            const int tiles = two ? 2 : 1;
+            // K of step j is item 2j, V item 2j + 1, in ring order
+            int ks = 0, kp = 0, vs = 1, vp = 0;
+            auto next = [&](int &st, int &phase) {
+                st += 2;
+                if (st >= RING)
+                    st -= RING, phase ^= 1;
+            };
+            bool begun = true;
+            for (int w = 0; w < tiles && begun; ++w)
+                begun = wait(&bars->q_full[w], 0);
+            if (begun && wait(&bars->kv_full[0], 0)) {
+                for (int w = 0; w < tiles; ++w)
+                    scores(w, 0);
+                commit(&bars->kv_empty[0]);
             }
-        }
-        for (int w = 0; w < 2; ++w)
-            tc::commit(&bars->o_full[w]);
-        // every MMA has finished before the tensor memory goes
-        (void)mbar_wait(&bars->o_full[0], 0, p.wait_limit_ns);
+            for (int j = 0; j < steps && !failed; ++j) {
+                next(ks, kp);
+                if (!wait(&bars->kv_full[vs], vp))
+                    break;
+                for (int w = 0; w < tiles; ++w) {
+                    if (!wait(&bars->p_half[w], j & 1))
+                        break;
+                    values(w, vs, j, 0);
+                    if (!wait(&bars->p_full[w], j & 1))
+                        break;
+                    values(w, vs, j, 1);
+                    if (w == tiles - 1)
+                        commit(&bars->kv_empty[vs]);
+                    if (j + 1 < steps) {
+                        if (w == 0 && !wait(&bars->kv_full[ks], kp))
+                            break;
+                        scores(w, ks);
+                        if (w == tiles - 1)
+                            commit(&bars->kv_empty[ks]);
+                    }
+                }
+                next(vs, vp);
+            }
+            for (int w = 0; w < 2; ++w)
+                commit(&bars->o_full[w]);
+            // every MMA has finished before the tensor memory goes
+            (void)tc::wait(&bars->o_full[0], 0, p.wait_limit_ns);
         }
     }
     if (failed)
@@ -507,34 +576,49 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
     __syncwarp();
     tc::fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        tc::cluster_sync();
     if (warp == 8) {
         tc::fence_after();
-        tc::dealloc(tmem, kCols);
+        if constexpr (PAIR)
+            tc::dealloc_pair(tmem, kCols);
+        else
+            tc::dealloc(tmem, kCols);
     }
+}
+
+template <int D, bool FP8, bool PAIR> cudaError_t launch_tiles(const KvAttendParams &p, cudaStream_t stream)
+{
+    using S = TileShape<D, PAIR>;
+    auto kern = kv_attend_tiles_kernel<D, FP8, PAIR>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((PAIR ? 2 : 1) * p.batch.seqs * p.cache.kv_heads * p.row_tiles * p.splits));
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 } // namespace
 
 cudaError_t launch_kv_attend_tiles(const KvAttendParams &p, cudaStream_t stream)
 {
-    const bool wide = p.cache.d == 128;
-    auto kern = wide ? (p.cache.fp8 ? kv_attend_tiles_kernel<128, true> : kv_attend_tiles_kernel<128, false>)
-                     : (p.cache.fp8 ? kv_attend_tiles_kernel<64, true> : kv_attend_tiles_kernel<64, false>);
-    const size_t smem = wide ? TileShape<128>::kSmem : TileShape<64>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.batch.seqs * p.cache.kv_heads * p.row_tiles * p.splits));
-    cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    if (p.cache.d == 64)
+        return p.cache.fp8 ? launch_tiles<64, true, false>(p, stream) : launch_tiles<64, false, false>(p, stream);
+    if (kv_attend_pairs(p))
+        return p.cache.fp8 ? launch_tiles<128, true, true>(p, stream) : launch_tiles<128, false, true>(p, stream);
+    return p.cache.fp8 ? launch_tiles<128, true, false>(p, stream) : launch_tiles<128, false, false>(p, stream);
 }
 
 } // namespace ss24

@@ -9,6 +9,39 @@
 namespace ss24 {
 namespace tc {
 
+// Waits for the barrier's phase with the given parity; false if that takes
+// longer than limit_ns. CLUSTER: the other CTA of a pair arrives on it too. The
+// timer is looked at late: reading it takes longer than most waits here last.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+    uint64_t t0 = 0;
+    for (int n = 0;; ++n) {
+        uint32_t ok;
+        if constexpr (CLUSTER)
+            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                         " selp.u32 %0, 1, 0, p;\n}\n"
+                         : "=r"(ok)
+                         : "r"(smem_u32(bar)), "r"(parity)
+                         : "memory");
+        else
+            ok = mbar_try_wait(bar, parity);
+        if (ok)
+            return true;
+        if (n >= 64 && n % 64 == 0) {
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0)
+                t0 = t;
+            else if (t - t0 > limit_ns)
+                return false;
+        }
+    }
+}
+
+// The warp's number, and a value that is the same in all its lanes, in a form
+// the compiler takes as uniform.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
+
 // Shared-memory matrix descriptor: start address, leading and stride byte
 // offsets (16-byte units), version 1, 128-byte swizzle.
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
@@ -42,37 +75,46 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // Generic-proxy writes to shared memory become visible to the tensor cores.
 __device__ __forceinline__ void fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void commit(uint64_t *bar)
+__device__ __forceinline__ void commit(uint64_t *bar, bool lead)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+                 " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+                 "r"(static_cast<uint32_t>(lead))
                  : "memory");
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// MMAs and commits are issued by the lane with `lead` set, but by code that the
+// whole warp runs: descriptors then stay in uniform registers. In a branch of
+// one lane each operand moves there first, which measured 76 cycles an MMA of 64.
+
 // D[tmem] (+)= A[smem] B[smem], INT8 x INT8 -> INT32
-__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                         bool lead)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(lead))
                  : "memory");
 }
 
 // D[tmem] (+)= A[smem] B[smem], fp16 x fp16 -> binary32
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                         bool lead)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(lead))
                  : "memory");
 }
 // the same with A in tensor memory (two values of k per 32-bit column)
-__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                         bool lead)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(lead))
                  : "memory");
 }
 
@@ -140,10 +182,13 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrival on a barrier of the cluster (an address from cluster_addr).
+// Arrival on a barrier of the cluster (an address from cluster_addr). What it
+// hands over went through a proxy or tcgen05 fence of its own before: a release
+// at cluster scope, which also waits for the thread's global loads, measured
+// 1000 cycles an arrival in the attention kernel.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ void alloc_pair(uint32_t *dst_smem, uint32_t cols)
 {
@@ -158,18 +203,36 @@ __device__ __forceinline__ void dealloc_pair(uint32_t taddr, uint32_t cols)
 }
 // Arrives on the barrier at `bar`'s offset in both CTAs once the MMAs issued
 // before it have finished.
-__device__ __forceinline__ void commit_pair(uint64_t *bar)
+__device__ __forceinline__ void commit_pair(uint64_t *bar, bool lead)
 {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+                 " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
                      smem_u32(bar)),
-                 "h"(static_cast<uint16_t>(3))
+                 "h"(static_cast<uint16_t>(3)), "r"(static_cast<uint32_t>(lead))
                  : "memory");
 }
-__device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                         bool lead)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(lead))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                         bool lead)
+{
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(lead))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_f16_ta_pair(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                         bool lead)
+{
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(lead))
                  : "memory");
 }
 // A box into this CTA's shared memory, completing on a barrier of the pair (an
