@@ -150,13 +150,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         int it = 0, phase = 0, n = 0;
         for (int64_t i = pair; i < tiles && !failed; i += pairs, ++n) {
             const int a = n & 1;
-            if (!tc::wait<true>(&bars->acc_empty[a], ((n >> 1) & 1) ^ 1, p.wait_limit_ns)) {
+            if (!tc::wait(&bars->acc_empty[a], ((n >> 1) & 1) ^ 1, p.wait_limit_ns)) {
                 failed = true;
                 break;
             }
             tc::fence_after();
             for (int kt = 0; kt < nk; ++kt) {
-                if (!tc::wait<true>(&bars->full[it], phase, p.wait_limit_ns)) {
+                if (!tc::wait(&bars->full[it], phase, p.wait_limit_ns)) {
                     failed = true;
                     break;
                 }

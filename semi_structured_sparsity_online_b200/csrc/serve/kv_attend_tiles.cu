@@ -42,7 +42,7 @@ template <int D, bool PAIR> struct TileShape {
     static constexpr int kKRows = PAIR ? kKeys / 2 : kKeys; // keys of K in this CTA
     static constexpr int kVCols = PAIR ? D / 2 : D;         // elements of V in this CTA
     static constexpr int kRing = PAIR ? 8 : 4;              // fp16 stages: K and V of a step take one each
-    static constexpr int kRaw = PAIR ? 3 : 2;               // stages of codes on their way from the pages
+    static constexpr int kRaw = PAIR ? 4 : 2;               // stages of codes on their way from the pages
     static constexpr int kScaleRing = kRing / 2 + 2;        // steps of page scales
     static constexpr uint32_t kQ = 128 * D * 2;             // a row tile of q
     static constexpr uint32_t kStage = kKRows * D * 2;      // equals kKeys * kVCols * 2
@@ -120,9 +120,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
     grid_dependency_wait();
 
     int32_t first, count, len;
-    const bool fine = kv_sequence(p.batch, s, p.err, &first, &count, &len);
+    const bool known = kv_sequence(p.batch, s, p.err, &first, &count, &len);
     const int64_t row0 = tile * ROWS, rows = static_cast<int64_t>(count) * p.group;
-    if (!fine || row0 >= rows)
+    if (!known || row0 >= rows)
         return;
     // MMA row tile w holds rows 128 CTAS w on; the CTA of rank r its r-th 128
     const int live = static_cast<int>(rows - row0 < ROWS ? rows - row0 : ROWS);
@@ -355,130 +355,137 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
         constexpr int RPW[2] = {32 / CPR[0], 32 / CPR[1]};
         constexpr int GROUPS = S::kKRows / RPW[0]; // the same for V
         constexpr int ITERS = (GROUPS + kConvWarps - 1) / kConvWarps;
+        constexpr int AHEAD = S::kRaw / 2;
         static_assert(kKeys / RPW[1] == GROUPS, "K and V items have one size");
         const int cw = warp - 9;
-        const int kr[2] = {lane / CPR[0], lane / CPR[1]}, cc[2] = {lane % CPR[0], lane % CPR[1]};
+        // A lane's key and chunk: 8 neighbouring lanes write 4 chunks of two
+        // neighbouring rows, whose swizzled places fall on different banks.
+        int kr[2], cc[2];
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            kr[kv] = CPR[kv] == 8 ? (lane >> 2) & 3 : lane >> 2;
+            cc[kv] = CPR[kv] == 8 ? (lane & 3) + (lane >> 4 << 2) : lane & 3;
+        }
         const int32_t *table = p.batch.table + s * p.batch.table_ld;
-        const int items = 2 * steps;
         const uint32_t raw = skv + RING * S::kStage + 16 * lane;
-        // Group g of this warp's iteration; beyond the last group there is none.
+        const int32_t end = static_cast<int32_t>(ke), begin = static_cast<int32_t>(kb);
+        // This warp's group in an iteration; beyond the last group there is none.
         auto group = [&](int it) { return it * kConvWarps + cw; };
-        auto page_at = [&](int32_t key) { return key < ke ? __ldg(table + (key >> p.cache.log2_page)) : -2; };
-        auto checked = [&](int32_t id) { // -2: no keys there
-            if (id >= p.cache.pages || id == -1 || id < -2) {
-                atomicCAS(p.err, 0, kErrPage);
-                return -2;
-            }
-            return id;
+        // Items come in the order K0, K1, V0, K2, V1, ...: when V of a step is there,
+        // K of the next is too, and the issuing lane waits once for both.
+        auto raw_at = [&](int j, int kv) {
+            const int n = kv == 1 ? 2 * j + 2 : j > 0 ? 2 * j - 1 : 0;
+            return raw + (n & (S::kRaw - 1)) * S::kCodes;
         };
-        // The key of this lane in iteration `it` of step j, K (0) or V (1).
-        auto key_at = [&](int j, int kv, int it) {
-            return static_cast<int32_t>(kb) + j * kKeys + (kv == 0 ? static_cast<int32_t>(rank) * S::kKRows : 0) +
-                   group(it) * RPW[kv] + kr[kv];
+        // Lanes 0-7 look up the 16-key groups of a step: the cache row of the
+        // group's first key (-1: no keys), and for the first warp its scales. Page
+        // numbers are loaded a step ahead; the scales of the step before go to
+        // shared memory. K of a step is fetched before V of the step before it.
+        auto load_id = [&](int j) {
+            const int32_t key = begin + j * kKeys + 16 * lane;
+            return lane < 8 && key < end ? __ldg(table + (key >> p.cache.log2_page)) : -1;
+        };
+        int32_t id = load_id(0), row = -1, row_before = -1;
+        float s_k = 0.0f, s_v = -1.0f; // s_v < 0: no keys
+        auto next_rows = [&](int j) {
+            if (cw == 0 && lane < 8 && j > 0) {
+                const float sv = fmaxf(s_v, 0x1p-100f);
+                scales[((j - 1) % S::kScaleRing) * 8 + lane] =
+                    s_v < 0.0f ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
+                               : make_float4(s_k, log2f(sv), __frcp_rn(sv), 0.0f);
+            }
+            const int32_t key = begin + j * kKeys + 16 * lane;
+            const bool there = lane < 8 && key < end, on = there && id >= 0 && id < p.cache.pages;
+            if (there && !on)
+                atomicCAS(p.err, 0, kErrPage);
+            const int32_t ph = on ? id * p.cache.kv_heads + h : 0;
+            row_before = row;
+            row = on ? (ph << p.cache.log2_page) + (key & (p.cache.page - 1)) : -1;
+            if (cw == 0) {
+                s_k = __ldg(p.cache.scales[0] + ph);
+                s_v = on ? __ldg(p.cache.scales[1] + ph) : -1.0f;
+            }
+            id = load_id(j + 1);
         };
         // Codes travel by asynchronous copies, kRaw items ahead; a thread reads
         // back only what it copied itself. Keys past the end and pages outside
-        // the cache are zeros. Page numbers are loaded a step before they are used.
-        int32_t ids[2][ITERS];
-        auto load_ids = [&](int j, int kv) {
-#pragma unroll
-            for (int it = 0; it < ITERS; ++it)
-                ids[kv][it] = group(it) < GROUPS ? page_at(key_at(j, kv, it)) : -2;
-        };
-        auto fetch = [&](int item, int slot, int kv) { // kv = item & 1
-            if (item < items) {
+        // the cache are zeros.
+        auto fetch = [&](int j, int kv) {
+            if (j < steps) {
                 const uint8_t *codes = p.cache.codes[kv] + 16 * cc[kv] + (kv == 1 ? rank * S::kVCols : 0);
 #pragma unroll
                 for (int it = 0; it < ITERS; ++it) {
-                    const int32_t id = checked(ids[kv][it]);
-                    const int64_t at = ((static_cast<int64_t>(id) * p.cache.kv_heads + h) << p.cache.log2_page) +
-                                       (key_at(item >> 1, kv, it) & (p.cache.page - 1));
+                    // the key's place in the step
+                    const int32_t at = (kv == 0 ? static_cast<int32_t>(rank) * S::kKRows : 0) + group(it) * RPW[kv] + kr[kv];
+                    const int32_t first_row = __shfl_sync(kFull, kv == 0 ? row : row_before, (at >> 4) & 7);
+                    const bool on = first_row >= 0 && begin + j * kKeys + at < end;
                     if (group(it) < GROUPS)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + slot * S::kCodes +
-                                                                                             group(it) * 512),
-                                     "l"(codes + (id < 0 ? 0 : at * D)), "r"(id < 0 ? 0 : 16));
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_at(j, kv) + group(it) * 512),
+                                     "l"(codes + static_cast<int64_t>(on ? first_row + (at & 15) : 0) * D),
+                                     "r"(on ? 16 : 0));
                 }
-                load_ids((item >> 1) + 1, kv);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        // s_k and s_v of 16-key group `lane` of a step (lanes 0-7 of the first
-        // warp), a step ahead; s_v < 0: no keys
-        const bool scaler = cw == 0 && lane < 8;
-        float s_k = 0.0f, s_v = -1.0f;
-        int32_t scale_id = -2;
-        auto load_scale_id = [&](int j) {
-            if (scaler)
-                scale_id = page_at(static_cast<int32_t>(kb) + j * kKeys + 16 * lane);
-        };
-        auto load_scales = [&] {
-            const bool on = scale_id >= 0 && scale_id < p.cache.pages;
-            const int64_t ph = on ? static_cast<int64_t>(scale_id) * p.cache.kv_heads + h : 0;
-            s_k = on ? __ldg(p.cache.scales[0] + ph) : 0.0f;
-            s_v = on ? __ldg(p.cache.scales[1] + ph) : -1.0f;
-        };
-        // One item: the codes in a raw slot to fp16 in a stage.
-        auto convert = [&](int raw_slot, uint32_t dst, int kv) {
+        // One item: the codes at src to fp16 in the stage at dst.
+        auto convert = [&](uint32_t src, uint32_t dst, int kv) {
             uint32_t u[ITERS][4];
 #pragma unroll
             for (int it = 0; it < ITERS; ++it)
                 if (group(it) < GROUPS)
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(u[it][0]), "=r"(u[it][1]), "=r"(u[it][2]), "=r"(u[it][3])
-                                 : "r"(raw + raw_slot * S::kCodes + group(it) * 512));
+                                 : "r"(src + group(it) * 512));
 #pragma unroll
             for (int it = 0; it < ITERS; ++it) {
                 uint32_t f[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     codes4_to_f16<FP8>(u[it][i], f[2 * i], f[2 * i + 1]);
-                // where 8 lanes write one row, the second four swap their two stores: all
-                // 8 lanes of a store phase then hit different banks
-                const bool odd = CPR[kv] == 8 && (cc[kv] & 4) != 0;
-                const uint32_t a0 = dst + chunk_at(kv == 0 ? S::kKAtom : S::kVAtom, group(it) * RPW[kv] + kr[kv], 2 * cc[kv]);
-                const uint32_t a1 = a0 ^ 16;
+                const uint32_t a = dst + chunk_at(kv == 0 ? S::kKAtom : S::kVAtom, group(it) * RPW[kv] + kr[kv], 2 * cc[kv]);
                 if (group(it) < GROUPS) {
-                    sts16(odd ? a1 : a0, odd ? f[4] : f[0], odd ? f[5] : f[1], odd ? f[6] : f[2], odd ? f[7] : f[3]);
-                    sts16(odd ? a0 : a1, odd ? f[0] : f[4], odd ? f[1] : f[5], odd ? f[2] : f[6], odd ? f[3] : f[7]);
+                    sts16(a, f[0], f[1], f[2], f[3]);
+                    sts16(a ^ 16, f[4], f[5], f[6], f[7]);
                 }
             }
         };
-        load_ids(0, 0);
-        load_ids(0, 1);
-        load_scale_id(0);
-        load_scales();
-        load_scale_id(1);
+        next_rows(0);
+        fetch(0, 0);
+        next_rows(1);
+        fetch(1, 0);
+        if constexpr (AHEAD == 2) {
+            fetch(0, 1);
+            next_rows(2);
+            fetch(2, 0);
+        }
+        int st = 0, phase = 1;
+        for (int i = 0; i <= steps && !failed; ++i) {
 #pragma unroll
-        for (int item = 0; item < S::kRaw; ++item)
-            fetch(item, item, item & 1);
-        int st = 0, phase = 1, raw_slot = 0;
-        for (int j = 0; j < steps && !failed; ++j) {
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
+            for (int kv = 0; kv < 2; ++kv) { // K of step i, V of step i - 1
+                const int j = i - kv;
+                if (j < 0 || j >= steps)
+                    continue;
                 if (!tc::wait(&bars->kv_empty[st], phase, p.wait_limit_ns)) {
                     failed = true;
                     break;
                 }
-                asm volatile("cp.async.wait_group %0;" ::"n"(S::kRaw - 1) : "memory");
-                convert(raw_slot, skv + st * S::kStage, kv);
-                if (kv == 0 && scaler) {
-                    // with a step's K, the scales of its 16-key groups
-                    const float sv = fmaxf(s_v, 0x1p-100f);
-                    scales[(j % S::kScaleRing) * 8 + lane] =
-                        s_v < 0.0f ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-                                   : make_float4(s_k, log2f(sv), __frcp_rn(sv), 0.0f);
-                }
+                // the last V has no K between it and the V before
+                if (kv == 1 && i == steps)
+                    asm volatile("cp.async.wait_group %0;" ::"n"(S::kRaw - 2) : "memory");
+                else
+                    asm volatile("cp.async.wait_group %0;" ::"n"(S::kRaw - 1) : "memory");
+                if (kv == 0 && j > 0)
+                    next_rows(j + AHEAD);
+                convert(raw_at(j, kv), skv + st * S::kStage, kv);
                 tc::fence_proxy();
                 arrive(&bars->kv_full[st]);
-                if (kv == 0 && scaler) {
-                    load_scales();
-                    load_scale_id(j + 2);
-                }
-                fetch(2 * j + kv + S::kRaw, raw_slot, (kv + S::kRaw) & 1);
+                // the item kRaw on takes the slot
+                if (kv == 0 && j == 0)
+                    fetch(AHEAD - 1, 1);
+                else
+                    fetch(j + AHEAD, kv);
                 if (++st == RING)
                     st = 0, phase ^= 1;
-                if (++raw_slot == S::kRaw)
-                    raw_slot = 0;
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             // ---- MMAs -----------------------------------------------------------
             constexpr uint32_t kIS = f16_idesc(128 * CTAS, kKeys, false), kIO = f16_idesc(128 * CTAS, D, true);
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                const bool ok = tc::wait<PAIR>(bar, parity, p.wait_limit_ns);
+                const bool ok = tc::wait(bar, parity, p.wait_limit_ns);
                 tc::fence_after();
                 failed = __any_sync(kFull, !ok);
                 return !failed;
@@ -500,12 +507,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 else
                     tc::commit(bar, lead);
             };
+            const uint32_t q_low = tc::desc_low_kmajor(sq), k_low = tc::desc_low_kmajor(skv);
+            const uint32_t v_low = tc::desc_low_mnmajor(skv, S::kVAtom);
             auto scores = [&](int w, int st) {
-                const uint32_t q = sq + w * S::kQ, k = skv + st * S::kStage;
+                const uint32_t q = q_low + w * (S::kQ >> 4), k = k_low + st * (S::kStage >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint64_t a = tc::desc_kmajor(q + (ks >> 2) * S::kQAtom + (ks & 3) * 32);
-                    const uint64_t b = tc::desc_kmajor(k + (ks >> 2) * S::kKAtom + (ks & 3) * 32);
+                    const uint64_t a = tc::desc(q + (ks >> 2) * (S::kQAtom >> 4) + (ks & 3) * 2);
+                    const uint64_t b = tc::desc(k + (ks >> 2) * (S::kKAtom >> 4) + (ks & 3) * 2);
                     if constexpr (PAIR)
                         tc::mma_f16_pair(tmem + 128 * w, a, b, kIS, ks > 0, lead);
                     else
@@ -515,10 +524,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             };
             // the first or second half of a step's keys
             auto values = [&](int w, int st, int j, int half) {
-                const uint32_t v = skv + st * S::kStage;
+                const uint32_t v = v_low + st * (S::kStage >> 4);
 #pragma unroll
                 for (int ks = 4 * half; ks < 4 * half + 4; ++ks) {
-                    const uint64_t b = tc::desc_mnmajor(v + ks * 2048, S::kVAtom);
+                    const uint64_t b = tc::desc(v + ks * (2048 >> 4));
                     const uint32_t a = tmem + 128 * w + 8 * ks, d = tmem + 256 + 128 * w;
                     if constexpr (PAIR)
                         tc::mma_f16_ta_pair(d, a, b, kIO, j > 0 || ks > 0, lead);
@@ -527,43 +536,46 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 }
             };
             const int tiles = two ? 2 : 1;
-            // K of step j is item 2j, V item 2j + 1, in ring order
-            int ks = 0, kp = 0, vs = 1, vp = 0;
-            auto next = [&](int &st, int &phase) {
-                st += 2;
-                if (st >= RING)
-                    st -= RING, phase ^= 1;
+            int next = 0, phase = 0; // the next item's stage
+            auto advance = [&] {
+                if (++next == RING)
+                    next = 0, phase ^= 1;
             };
-            bool begun = true;
-            for (int w = 0; w < tiles && begun; ++w)
-                begun = wait(&bars->q_full[w], 0);
-            if (begun && wait(&bars->kv_full[0], 0)) {
+            bool fine = true;
+            for (int w = 0; w < tiles && fine; ++w)
+                fine = wait(&bars->q_full[w], 0);
+            fine = fine && wait(&bars->kv_full[0], 0);
+            if (fine) {
                 for (int w = 0; w < tiles; ++w)
                     scores(w, 0);
                 commit(&bars->kv_empty[0]);
             }
-            for (int j = 0; j < steps && !failed; ++j) {
-                next(ks, kp);
-                if (!wait(&bars->kv_full[vs], vp))
-                    break;
-                for (int w = 0; w < tiles; ++w) {
-                    if (!wait(&bars->p_half[w], j & 1))
+            advance();
+            for (int j = 0; j < steps && fine; ++j) {
+                const bool more = j + 1 < steps;
+                const int ks = next;
+                if (more)
+                    advance();
+                const int vs = next;
+                fine = wait(&bars->kv_full[vs], phase); // and K before it
+                advance();
+                for (int w = 0; w < tiles && fine; ++w) {
+                    fine = wait(&bars->p_half[w], j & 1);
+                    if (!fine)
                         break;
                     values(w, vs, j, 0);
-                    if (!wait(&bars->p_full[w], j & 1))
+                    fine = wait(&bars->p_full[w], j & 1);
+                    if (!fine)
                         break;
                     values(w, vs, j, 1);
                     if (w == tiles - 1)
                         commit(&bars->kv_empty[vs]);
-                    if (j + 1 < steps) {
-                        if (w == 0 && !wait(&bars->kv_full[ks], kp))
-                            break;
+                    if (more) {
                         scores(w, ks);
                         if (w == tiles - 1)
                             commit(&bars->kv_empty[ks]);
                     }
                 }
-                next(vs, vp);
             }
             for (int w = 0; w < 2; ++w)
                 commit(&bars->o_full[w]);

@@ -10,23 +10,13 @@ namespace ss24 {
 namespace tc {
 
 // Waits for the barrier's phase with the given parity; false if that takes
-// longer than limit_ns. CLUSTER: the other CTA of a pair arrives on it too. The
-// timer is looked at late: reading it takes longer than most waits here last.
-template <bool CLUSTER = false>
+// longer than limit_ns. The timer is looked at late: reading it takes longer
+// than most waits here last.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
 {
     uint64_t t0 = 0;
     for (int n = 0;; ++n) {
-        uint32_t ok;
-        if constexpr (CLUSTER)
-            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-                         " selp.u32 %0, 1, 0, p;\n}\n"
-                         : "=r"(ok)
-                         : "r"(smem_u32(bar)), "r"(parity)
-                         : "memory");
-        else
-            ok = mbar_try_wait(bar, parity);
-        if (ok)
+        if (mbar_try_wait(bar, parity))
             return true;
         if (n >= 64 && n % 64 == 0) {
             const uint64_t t = global_timer_ns();
@@ -42,23 +32,24 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint64_t li
 // the compiler takes as uniform.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
 
-// Shared-memory matrix descriptor: start address, leading and stride byte
-// offsets (16-byte units), version 1, 128-byte swizzle.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo)
+// Shared-memory matrix descriptor of a 128-byte swizzled operand: its high word
+// is the same for all (groups of 8 rows 1024 bytes apart, version 1, the
+// swizzle), its low word holds the address and the leading byte offset in
+// 16-byte units, so that a step along the operand is an addition to it.
+__device__ __forceinline__ uint64_t desc(uint32_t low)
 {
-    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | static_cast<uint64_t>(lbo & 0x3fffu) << 16 |
-           static_cast<uint64_t>(sbo & 0x3fffu) << 32 | static_cast<uint64_t>(1u) << 46 |
-           static_cast<uint64_t>(2u) << 61;
+    constexpr uint32_t kHigh = 64u | 1u << 14 | 2u << 29;
+    return static_cast<uint64_t>(kHigh) << 32 | low;
 }
+// K-major operand: rows of 128 bytes.
+__device__ __forceinline__ uint32_t desc_low_kmajor(uint32_t addr) { return (addr >> 4) + (1u << 16); }
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t addr) { return desc(desc_low_kmajor(addr)); }
 // MN-major operand (the MMA's m or n contiguous): rows of k with 128 bytes of
-// n each, groups of 8 rows of k 1024 bytes apart, the next 128 bytes of n
-// n_stride bytes on.
-__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t addr, uint32_t n_stride)
+// n each, the next 128 bytes of n n_stride bytes on.
+__device__ __forceinline__ uint32_t desc_low_mnmajor(uint32_t addr, uint32_t n_stride)
 {
-    return desc_sw128(addr, n_stride >> 4, 64);
+    return (addr >> 4) + (n_stride >> 4 << 16);
 }
-// K-major operand: rows of 128 bytes, groups of 8 rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_kmajor(uint32_t addr) { return desc_sw128(addr, 1, 64); }
 
 __device__ __forceinline__ void alloc(uint32_t *dst_smem, uint32_t cols)
 {
