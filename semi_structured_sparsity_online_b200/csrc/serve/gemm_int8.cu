@@ -111,7 +111,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     tc::cluster_sync();
     tc::fence_after();
-    const uint32_t tmem = *tmem_base;
+    const uint32_t tmem = tc::uniform(*tmem_base);
     grid_dependents_launch();
     grid_dependency_wait();
     bool failed = false;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *tmem_base;
+    const uint32_t tmem = tc::uniform(*tmem_base);
     grid_dependents_launch();
     grid_dependency_wait();
     bool failed = false;

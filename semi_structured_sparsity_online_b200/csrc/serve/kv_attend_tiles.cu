@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
     if constexpr (PAIR)
         tc::cluster_sync();
     tc::fence_after();
-    const uint32_t tmem = *tmem_base;
+    const uint32_t tmem = tc::uniform(*tmem_base);
     bool failed = false;
     // a warp's arrival on a barrier that the issuing lane waits on
     auto arrive = [&](uint64_t *bar) {
@@ -227,49 +227,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 const bool edge = key0 + kKeys > low;
                 const float4 *sc = scales + (j % S::kScaleRing) * 8;
                 uint32_t v[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tc::ld32(ts + 32 * c, v[c]);
-                tc::wait_ld();
-                if (edge) {
+                auto load = [&] {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
+                        tc::ld32(ts + 32 * c, v[c]);
+                    tc::wait_ld();
+                };
+                // the largest exponent in the row's 128 keys
+                auto largest = [&] {
+                    float mx = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (key0 + 32 * c + i >= limit)
-                                v[c][i] = 0xff800000u; // -infinity
-                }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const uint32_t *y = &v[g >> 1][16 * (g & 1)];
-                    float x = max3(y[0], y[1], y[2]), z = max3(y[3], y[4], y[5]);
-                    x = max3(__float_as_uint(x), y[6], y[7]), z = max3(__float_as_uint(z), y[8], y[9]);
-                    x = max3(__float_as_uint(x), y[10], y[11]), z = max3(__float_as_uint(z), y[12], y[13]);
-                    x = fmaxf(max3(__float_as_uint(x), y[14], y[15]), z);
-                    mx = fmaxf(mx, fmaf(x, factor(sc[g].x), sc[g].y));
-                }
-                if (__any_sync(kFull, mx > m + 8.0f)) {
-                    const float mn = fmaxf(m, mx), f = exp2_approx(m - mn);
-                    m = mn;
-                    l *= f;
-                    if (j > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t v[32];
-                            tc::ld32(to + c, v);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                            tc::st32(to + c, v);
-                        }
-                        tc::wait_st();
+                    for (int g = 0; g < 8; ++g) {
+                        const uint32_t *y = &v[g >> 1][16 * (g & 1)];
+                        float x = max3(y[0], y[1], y[2]), z = max3(y[3], y[4], y[5]);
+                        x = max3(__float_as_uint(x), y[6], y[7]), z = max3(__float_as_uint(z), y[8], y[9]);
+                        x = max3(__float_as_uint(x), y[10], y[11]), z = max3(__float_as_uint(z), y[12], y[13]);
+                        x = fmaxf(max3(__float_as_uint(x), y[14], y[15]), z);
+                        mx = fmaxf(mx, fmaf(x, factor(sc[g].x), sc[g].y));
                     }
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
+                    return mx;
+                };
+                // Weights of keys 32 c on, in pairs over v[c][0 .. 15]; their sum over the
+                // V scales is returned.
+                auto weights = [&](int c) {
+                    float total = 0.0f;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const float4 f = sc[2 * c + g];
@@ -280,20 +261,59 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                         for (int i = 0; i < 16; i += 2) {
                             const f32x2 x = fma2(
                                 pack2(__uint_as_float(v[c][16 * g + i]), __uint_as_float(v[c][16 * g + i + 1])), af2, bm2);
-                            const float x0 = exp2_approx(lo2(x)), x1 = exp2_approx(hi2(x));
-                            sum = add2(sum, pack2(x0, x1));
-                            pk[8 * g + i / 2] = pack_f16(x0, x1);
+                            const f32x2 e = pack2(exp2_approx(lo2(x)), exp2_approx(hi2(x)));
+                            sum = add2(sum, e);
+                            v[c][8 * g + i / 2] = pack_f16(lo2(e), hi2(e));
                         }
-                        l = fmaf(lo2(sum) + hi2(sum), f.z, l);
+                        total = fmaf(lo2(sum) + hi2(sum), f.z, total);
                     }
+                    return total;
+                };
+                auto store = [&](int c) {
+                    const uint32_t(&pk)[16] = *reinterpret_cast<const uint32_t(*)[16]>(v[c]);
                     tc::st16(ts + 16 * c, pk);
-                    if (c & 1) {
-                        // half of the step's weights: its products may start
+                };
+                load();
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (key0 + 32 * c + i >= limit)
+                                v[c][i] = 0xff800000u; // -infinity
+                }
+                const float mx = largest();
+                if (__any_sync(kFull, mx > m + 8.0f)) {
+                    const float mn = fmaxf(m, mx), f = exp2_approx(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tc::ld32(to + c, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tc::st32(to + c, o);
+                        }
                         tc::wait_st();
-                        tc::fence_before();
-                        arrive(c == 1 ? &bars->p_half[w] : &bars->p_full[w]);
                     }
                 }
+                float sum = weights(0) + weights(1);
+                store(0);
+                store(1);
+                // half of the step's weights: their products may start
+                tc::wait_st();
+                tc::fence_before();
+                arrive(&bars->p_half[w]);
+                l += sum + weights(2) + weights(3);
+                store(2);
+                store(3);
+                tc::wait_st();
+                tc::fence_before();
+                arrive(&bars->p_full[w]);
             }
 
             // ---- the row's output -------------------------------------------------
@@ -559,7 +579,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 const int vs = next;
                 fine = wait(&bars->kv_full[vs], phase); // and K before it
                 advance();
-                for (int w = 0; w < tiles && fine; ++w) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (w >= tiles || !fine)
+                        break;
                     fine = wait(&bars->p_half[w], j & 1);
                     if (!fine)
                         break;
