@@ -587,13 +587,14 @@ void kv_attend_plan(KvAttendParams *p)
     const int64_t tile = wide(*p) ? pair * kTileRows : narrow(*p) ? 8 : 16;
     p->row_tiles = static_cast<int32_t>(ceil_div(rows, tile));
     const int64_t ctas = p->batch.seqs * p->cache.kv_heads * p->row_tiles;
-    // Parts of the key axis: as many CTAs as run at once and no more, of 256 keys
+    // Parts of the key axis: as many CTAs as run at once and no more, of 512 keys
     // or more. A second wave costs its start and end (131072 keys, 8 heads, 8 rows
-    // each: 53 us in one wave of 296, 58 in two, 68 in four); more parts than 256
-    // keys give cost as much as they save (500 keys: 7.3 - 7.9 us either way).
+    // each: 53 us in one wave of 296, 58 in two, 68 in four). Smaller parts save
+    // little on the device and cost the join's launch (500 keys: 7.4 us in one
+    // part, 7.8 in two; 1000 keys: 9.4 in two, 8.2 in four).
     const int64_t step = 128;
     int64_t splits = ctas > 0 ? 148 * (wide(*p) ? 1 : 2) / (pair * ctas) : 1;
-    const int64_t most = ceil_div(len, 2 * step);
+    const int64_t most = ceil_div(len, 4 * step);
     splits = splits > most ? most : splits;
     splits = splits < 1 ? 1 : splits > kMaxParts ? kMaxParts : splits;
     p->split_keys = static_cast<int32_t>(ceil_div(ceil_div(len, splits), step) * step);

@@ -479,6 +479,9 @@ def sparse_gemm_fp8(a, b, y=None, ws=None, stream=None):
 # microseconds: they check with few attribute reads, enter no context that is
 # already current and ask for the stream's raw handle only.
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _same_device(index, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != index:
@@ -490,14 +493,14 @@ def _enqueue(index, stream, name, *args):
     or that device's current stream."""
     if index < 0:
         raise ValueError(f"{name} needs CUDA tensors")
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    fn = getattr(lib(), name)
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    fn = getattr(_lib or lib(), name)
     if torch.cuda.current_device() == index:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(index):
             st = fn(*args, raw)
-    if st != OK:
+    if st:
         raise SS24Error(st, name)
 
 
@@ -529,7 +532,7 @@ def gemm_int8(a, b, dtype=torch.bfloat16, y=None, ws=None, stream=None):
     if y is None:
         if dtype is not torch.bfloat16 and dtype is not torch.float32:
             raise TypeError("y must be bfloat16 or float32")
-        y, ld = av.new_empty((m, n), dtype=dtype), n
+        y, ld = torch.empty((m, n), dtype=dtype, device=av.device), n
     else:
         if y.dtype is not torch.bfloat16 and y.dtype is not torch.float32:
             raise TypeError("y must be bfloat16 or float32")
@@ -645,24 +648,28 @@ def kv_attention(q, cache, page_table, starts, lengths, scale=None, causal=True,
     d = c.head_dim
     qr = _head_rows(q, "q", d)
     b = _kv_batch(cache, q.shape[0], page_table, starts, lengths, max_new, max_len)
+    heads = qr.heads
     if out is None:
-        out = q.new_empty(q.shape)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        outr = HeadRows(out.data_ptr(), qr.dtype, heads, heads * d, d)
+    else:
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        outr = _head_rows(out, "out", d)
     if lse is True:
-        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
-    elif lse is False:
+        lse = q.new_empty((b.tokens, heads), dtype=torch.float32)
+    elif lse is False or lse is None:
         lse = None
     elif lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [tokens, q_heads]")
-    outr = _head_rows(out, "out", d)
     index = cache["k"].get_device()
     _same_device(index, q, out, lse)
     ws = _workspace(ws, q)
-    n = lib().ss24_kv_attention_scratch_bytes(c, b, qr.heads)
-    scratch = q.new_empty((n,), dtype=torch.uint8) if n > 0 else None
+    n = lib().ss24_kv_attention_scratch_bytes(c, b, heads)
+    scratch = q.new_empty(n, dtype=torch.uint8) if n > 0 else None
     _enqueue(index, None, "ss24_kv_attention", qr, c, b, d ** -0.5 if scale is None else float(scale),
-             1 if causal else 0, outr, _ptr(lse), _ptr(scratch), max(n, 0), ws.ptr, ws.nbytes)
+             1 if causal else 0, outr, None if lse is None else lse.data_ptr(),
+             None if scratch is None else scratch.data_ptr(), max(n, 0), ws.ptr, ws.nbytes)
     return out if lse is None else (out, lse)
 
 
