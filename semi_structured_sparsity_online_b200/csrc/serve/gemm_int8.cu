@@ -246,7 +246,7 @@ template <int BN> struct Split {
     static constexpr uint32_t kStage = (kBM + BN) * kBK;
     static constexpr uint32_t kCols = BN < 32 ? 32 : BN;
     static constexpr size_t kSmem = 1024 + kStages * kStage + 128 + 4 * BN;
-    static_assert(kStages * kStage >= 4 * kBM * BN, "the stages hold a CTA's sums");
+    static_assert(kStages * kStage >= 4 * kBM * (BN < 16 ? 16 : BN), "the stages hold a part's sums");
 };
 
 template <int BN, typename Y>
@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(kSplitThreads)
     uint8_t *stages = align1024(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(stages + STAGES * S::kStage);
     uint64_t *empty = full + STAGES;
-    uint64_t *accbar = empty + STAGES;
-    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(accbar + 1);
-    float *sa = reinterpret_cast<float *>(accbar + 2);
+    uint64_t *accbar = empty + STAGES, *joined = accbar + 1;
+    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(accbar + 2);
+    float *sa = reinterpret_cast<float *>(accbar + 3);
 
     const int tid = threadIdx.x, warp = tc::uniform(tid >> 5), lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x % parts);
@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kSplitThreads)
             mbar_init(&empty[s], 1);
         }
         mbar_init(accbar, 1);
+        mbar_init(joined, 1);
         fence_barrier_init();
     }
     if (warp == 1)
@@ -348,9 +349,11 @@ __global__ void __launch_bounds__(kSplitThreads)
                     store_y(static_cast<Y *>(p.y) + (t0 + j0 + i) * p.ldy + c, v[i], sa[j0 + i], sb);
         }
     } else {
-        // this part's sums over the stages (all read by now): column j, channel
-        // tid at 4 (128 j + tid); then each CTA joins its share of the columns
-        const uint32_t sums = smem_u32(stages) + 4 * tid;
+        // This part's sums over the stages (all read by now), column j of channel c at
+        // 4 (128 j + c). Each CTA answers for a share of the columns; the others' sums of
+        // those are added to its own by bulk reductions between the CTAs' shared memories.
+        const int share = (cols + parts - 1) / parts;
+        const uint32_t sums = smem_u32(stages);
 #pragma unroll 1
         for (int j0 = 0; j0 < cols; j0 += 16) {
             uint32_t v[16];
@@ -358,26 +361,36 @@ __global__ void __launch_bounds__(kSplitThreads)
             tc::ld16(acc + j0, v);
             tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(sums + 512 * (j0 + i)), "r"(v[i]) : "memory");
+            for (int i = 0; i < 16; ++i) // up to 15 columns of the MMA's behind cols
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(sums + 512 * (j0 + i) + 4 * tid), "r"(v[i]) : "memory");
         }
+        const int mine = cols - rank * share < 0 ? 0 : cols - rank * share < share ? cols - rank * share : share;
+        if (tid == 0)
+            mbar_arrive_expect_tx(joined, static_cast<uint32_t>((parts - 1) * mine * 512));
+        tc::fence_proxy();
+        __syncthreads();
         tc::cluster_sync();
-        const int share = (cols + parts - 1) / parts;
-        const int j1 = (rank + 1) * share < cols ? (rank + 1) * share : cols;
-        for (int j = rank * share; j < j1; ++j) {
-            int sum = 0;
-            for (int r = 0; r < parts; ++r) {
-                int x;
-                asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                             : "=r"(x)
-                             : "r"(tc::cluster_addr(sums + 512 * j, r))
+        if (tid < parts && tid != rank) {
+            const int n = cols - tid * share < share ? cols - tid * share : share; // the other's columns
+            if (n > 0) {
+                const uint32_t from = sums + 512 * share * tid;
+                asm volatile("cp.reduce.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes.add.s32"
+                             " [%0], [%1], %2, [%3];" ::"r"(tc::cluster_addr(from, tid)),
+                             "r"(from), "r"(n * 512), "r"(tc::cluster_addr(smem_u32(joined), tid))
                              : "memory");
-                sum += x;
             }
-            if (on)
-                store_y(static_cast<Y *>(p.y) + (t0 + j) * p.ldy + c, static_cast<uint32_t>(sum), sa[j], sb);
         }
-        tc::cluster_sync(); // a CTA's sums stay until the others have read them
+        __syncwarp();
+        if (!tc::wait(joined, 0, p.wait_limit_ns))
+            failed = true;
+        for (int j = 0; j < mine; ++j) {
+            uint32_t sum;
+            const int col = rank * share + j;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sum) : "r"(sums + 512 * col + 4 * tid) : "memory");
+            if (on)
+                store_y(static_cast<Y *>(p.y) + (t0 + col) * p.ldy + c, sum, sa[col], sb);
+        }
+        tc::cluster_sync(); // a CTA's sums stay until the reductions have read them
     }
     if (failed)
         atomicCAS(p.err, 0, kErrGemmWait);
@@ -426,10 +439,11 @@ template <int BN> cudaError_t launch_split(const GemmInt8Params &p, cudaStream_t
     const int64_t tiles = ceil_div(p.n, kBM) * ceil_div(p.m, BN), nk = ceil_div(p.k, kBK);
     if (tiles > INT32_MAX / 8)
         return cudaErrorInvalidValue;
-    // parts of k: doubled while all CTAs still run at once and each keeps at
-    // least two stages of work
+    // Parts of k: doubled while all CTAs still run at once and each keeps eight
+    // stages of work. One token, 4096 x 4096: 4 parts (of eight stages) 5.1 us, 8
+    // parts 5.4, 1 part 9.4; 4096 channels of 14336: 8 parts 12.3, 4 parts 13.7.
     int parts = 1;
-    while (parts < 8 && tiles * parts * 2 <= Split<BN>::kPerSm * kSms && nk >= 4 * parts)
+    while (parts < 8 && tiles * parts * 2 <= Split<BN>::kPerSm * kSms && nk >= 16 * parts)
         parts *= 2;
     return launch_gemm(p.y_f32 ? gemm_int8_split_kernel<BN, float> : gemm_int8_split_kernel<BN, __nv_bfloat16>,
                        Split<BN>::kSmem, tiles * parts, kSplitThreads, parts, stream, mw, mx, p,
@@ -451,14 +465,17 @@ cudaError_t launch_pair(const GemmInt8Params &p, cudaStream_t stream)
 
 cudaError_t launch_gemm_int8(const GemmInt8Params &p, cudaStream_t stream)
 {
-    // pairs where their tiles occupy a good part of the SMs
+    // Pairs where their tiles occupy a good part of the SMs. Else the narrowest tile
+    // that holds the tokens; above 64 tokens 128 wide ones, which read the weight
+    // once, unless they are too few to keep the SMs busy (128 tokens, 1024 channels
+    // of 4096: 9.0 us, with 64 wide tiles 7.6; 14336 channels: 15.8 and 17.1).
     if (p.m > 128 && ceil_div(p.n, 2 * kBM) * ceil_div(p.m, kPairN) >= kSms / 4)
         return launch_pair(p, stream);
     if (p.m <= 16)
         return launch_split<16>(p, stream);
     if (p.m <= 32)
         return launch_split<32>(p, stream);
-    if (p.m <= 64)
+    if (p.m <= 64 || ceil_div(p.n, kBM) * ceil_div(p.m, 128) < 32)
         return launch_split<64>(p, stream);
     return launch_split<128>(p, stream);
 }
