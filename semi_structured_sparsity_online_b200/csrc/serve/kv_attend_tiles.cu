@@ -8,9 +8,11 @@
 //             shared memory in fp16, takes its row of S = q K^T from tensor
 //             memory, forms the weights and writes them back as fp16 over S;
 //             row maxima and sums need no shuffle
-//   8         one lane issues the MMAs: S (K-major operands) and O += P V with
-//             P in tensor memory and V as it lies (MN-major)
-//   9-15      codes of K and V from the pages to fp16 in shared memory, a ring
+//   8, 9      one lane each issues a row tile's MMAs: S (K-major operands) and
+//             O += P V with P in tensor memory and V as it lies (MN-major). An MMA
+//             takes some ten instructions to issue, 70 - 85 cycles between the other
+//             warps' of its scheduler, as long as it runs: hence two warps.
+//   10-15     codes of K and V from the pages to fp16 in shared memory, a ring
 //             of stages in the 128-byte swizzle that the MMA reads
 // PAIR: two CTAs of a cluster work on twice the rows with cta_group::2 MMAs.
 // Each brings half of every B operand (64 keys of K, 64 of the 128 elements of
@@ -20,11 +22,13 @@
 // conversion. The even CTA's lane issues for both; barriers that it waits on
 // are arrived on by both.
 //
-// The two row tiles take turns: while one warpgroup works on its S, the
-// tensor cores serve the other. A new S overwrites the weights of the step
-// before; MMAs of one thread run in order, and the commit behind S(j + 1) also
-// tells that P V of step j is done, so the output may be rescaled then. That
-// happens only when a row's bound M moves by more than 2^8.
+// A step's S is handled in two halves of 64 keys with barriers of their own:
+// while a row's thread works on one half, the tensor cores multiply the weights
+// of the other with V and form the next S in its place (MMAs of one thread run
+// in order, so a new S may overwrite the weights that the MMA before it read).
+// In whole steps a row tile's softmax and its MMAs waited for each other, 2400
+// and 1400 cycles of a step of 4100. The output is rescaled when a row's bound M
+// moves by more than 2^8, which waits for the other half's products first.
 #include "kv_attend.cuh"
 #include "tcgen05.cuh"
 
@@ -36,7 +40,7 @@ constexpr int kTileThreads = 512;
 // 512 threads start with 128 registers each; 2 x 128 x (176 + 80) is the same sum
 constexpr int kRegsRows = 176, kRegsRest = 80;
 constexpr int kKeys = 128;   // keys per step
-constexpr int kConvWarps = 7;
+constexpr int kConvWarps = 6;
 
 template <int D, bool PAIR> struct TileShape {
     static constexpr int kKRows = PAIR ? kKeys / 2 : kKeys; // keys of K in this CTA
@@ -81,7 +85,7 @@ __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c)
 
 constexpr int kMaxRing = 8;
 struct Bars {
-    uint64_t kv_full[kMaxRing], kv_empty[kMaxRing], q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
+    uint64_t kv_full[kMaxRing], kv_empty[kMaxRing], q_full[2], s_full[2][2], p_full[2][2], o_full[2];
 };
 
 // 16-byte chunk c (8 fp16) of row r in swizzled atoms of 128 bytes a row.
@@ -95,7 +99,15 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-template <int D, bool FP8, bool PAIR>
+// Key n of half h of a step, and V's first row of k step ks of it. A pair's CTAs
+// bring 32 of a half's keys each: of keys 0-63 of the step and of keys 64-127.
+template <bool PAIR> __device__ __forceinline__ constexpr int half_key(int h, int n)
+{
+    return PAIR ? (n < 32 ? 32 * h + n : 64 + 32 * h + (n - 32)) : 64 * h + n;
+}
+
+// COARSE: pages of 32 or more, so that 32 neighbouring keys share their scales.
+template <int D, bool FP8, bool PAIR, bool COARSE>
 __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const KvAttendParams p)
 {
     using S = TileShape<D, PAIR>;
@@ -138,13 +150,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
         // arrivals come from warps, of both CTAs
         for (int i = 0; i < RING; ++i) {
             mbar_init(&bars->kv_full[i], CTAS * kConvWarps);
-            mbar_init(&bars->kv_empty[i], 1);
+            mbar_init(&bars->kv_empty[i], two ? 2 : 1); // from the issuing warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], CTAS * 4);
-            mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_half[i], CTAS * 4);
-            mbar_init(&bars->p_full[i], CTAS * 4);
+            for (int half = 0; half < 2; ++half) {
+                mbar_init(&bars->s_full[i][half], 1);
+                mbar_init(&bars->p_full[i][half], CTAS * 4);
+            }
             mbar_init(&bars->o_full[i], 1);
         }
         fence_barrier_init();
@@ -212,108 +225,97 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             arrive(&bars->q_full[w]);
 
             const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-            const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
+            const uint32_t ts0 = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
             const int32_t low = __reduce_min_sync(kFull, limit);
             // never 0 (a page of zero keys, scale 0): 0 times a masked -infinity is NaN
             auto factor = [&](float s_k) { return fmaxf(s_k * fac, 0x1p-126f); };
+            constexpr int GS = COARSE ? 32 : 16, GN = 64 / GS; // keys that share scales, such groups
             float m = -1e30f, l = 0.0f;
-            for (int j = 0; j < steps; ++j) {
-                if (!tc::wait(&bars->s_full[w], j & 1, p.wait_limit_ns)) {
+            for (int i = 0; i < 2 * steps; ++i) {
+                const int j = i >> 1, half = i & 1;
+                if (!tc::wait(&bars->s_full[w][half], j & 1, p.wait_limit_ns)) {
                     failed = true;
                     break;
                 }
                 tc::fence_after();
+                const uint32_t ts = ts0 + 64 * half; // S, and the weights in its first half
                 const int32_t key0 = static_cast<int32_t>(kb) + j * kKeys;
-                const bool edge = key0 + kKeys > low;
                 const float4 *sc = scales + (j % S::kScaleRing) * 8;
-                uint32_t v[4][32];
-                auto load = [&] {
+                uint32_t v[64];
+                __syncwarp();
+                tc::ld32(ts, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+                tc::ld32(ts + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+                tc::wait_ld();
+                if (key0 + kKeys > low) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tc::ld32(ts + 32 * c, v[c]);
-                    tc::wait_ld();
-                };
-                // the largest exponent in the row's 128 keys
-                auto largest = [&] {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        const uint32_t *y = &v[g >> 1][16 * (g & 1)];
-                        float x = max3(y[0], y[1], y[2]), z = max3(y[3], y[4], y[5]);
-                        x = max3(__float_as_uint(x), y[6], y[7]), z = max3(__float_as_uint(z), y[8], y[9]);
-                        x = max3(__float_as_uint(x), y[10], y[11]), z = max3(__float_as_uint(z), y[12], y[13]);
-                        x = fmaxf(max3(__float_as_uint(x), y[14], y[15]), z);
-                        mx = fmaxf(mx, fmaf(x, factor(sc[g].x), sc[g].y));
-                    }
-                    return mx;
-                };
-                // Weights of keys 32 c on, in pairs over v[c][0 .. 15]; their sum over the
-                // V scales is returned.
-                auto weights = [&](int c) {
-                    float total = 0.0f;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float4 f = sc[2 * c + g];
-                        const float af = factor(f.x), bm = f.y - m;
-                        const f32x2 af2 = pack2(af, af), bm2 = pack2(bm, bm);
-                        f32x2 sum = pack2(0.0f, 0.0f);
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const f32x2 x = fma2(
-                                pack2(__uint_as_float(v[c][16 * g + i]), __uint_as_float(v[c][16 * g + i + 1])), af2, bm2);
-                            const f32x2 e = pack2(exp2_approx(lo2(x)), exp2_approx(hi2(x)));
-                            sum = add2(sum, e);
-                            v[c][8 * g + i / 2] = pack_f16(lo2(e), hi2(e));
-                        }
-                        total = fmaf(lo2(sum) + hi2(sum), f.z, total);
-                    }
-                    return total;
-                };
-                auto store = [&](int c) {
-                    const uint32_t(&pk)[16] = *reinterpret_cast<const uint32_t(*)[16]>(v[c]);
-                    tc::st16(ts + 16 * c, pk);
-                };
-                load();
-                if (edge) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (key0 + 32 * c + i >= limit)
-                                v[c][i] = 0xff800000u; // -infinity
+                    for (int k = 0; k < 64; ++k)
+                        if (key0 + half_key<PAIR>(half, k) >= limit)
+                            v[k] = 0xff800000u; // -infinity
                 }
-                const float mx = largest();
+                float4 f[GN];
+#pragma unroll
+                for (int g = 0; g < GN; ++g) {
+                    f[g] = sc[half_key<PAIR>(half, GS * g) >> 4];
+                    f[g].x = factor(f[g].x);
+                }
+                // the largest exponent in the row's 64 keys
+                float mx = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < GN; ++g) {
+                    const uint32_t *y = v + GS * g;
+                    float x = max3(y[0], y[1], y[2]), z = max3(y[3], y[4], y[5]);
+#pragma unroll
+                    for (int k = 6; k + 3 < GS; k += 4) {
+                        x = max3(__float_as_uint(x), y[k], y[k + 1]);
+                        z = max3(__float_as_uint(z), y[k + 2], y[k + 3]);
+                    }
+                    x = max3(__float_as_uint(x), y[GS - 2], y[GS - 1]);
+                    mx = fmaxf(mx, fmaf(fmaxf(x, z), f[g].x, f[g].y));
+                }
                 if (__any_sync(kFull, mx > m + 8.0f)) {
-                    const float mn = fmaxf(m, mx), f = exp2_approx(m - mn);
+                    const float mn = fmaxf(m, mx), scale = exp2_approx(m - mn);
                     m = mn;
-                    l *= f;
-                    if (j > 0) {
+                    l *= scale;
+                    if (i > 0) {
+                        // the half before: its products are done when the S behind them is (or,
+                        // in the last step, when the barrier that stands for it says so)
+                        if (!tc::wait(&bars->s_full[w][half ^ 1], (j + half) & 1, p.wait_limit_ns)) {
+                            failed = true;
+                            break;
+                        }
+                        tc::fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
                             tc::ld32(to + c, o);
                             tc::wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            for (int k = 0; k < 32; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * scale);
                             tc::st32(to + c, o);
                         }
                         tc::wait_st();
                     }
                 }
-                float sum = weights(0) + weights(1);
-                store(0);
-                store(1);
-                // half of the step's weights: their products may start
+                // the weights, in pairs over v[0 .. 31]; their sum over the V scales
+#pragma unroll
+                for (int g = 0; g < GN; ++g) {
+                    const float bm = f[g].y - m;
+                    const f32x2 af2 = pack2(f[g].x, f[g].x), bm2 = pack2(bm, bm);
+                    f32x2 sum = pack2(0.0f, 0.0f);
+#pragma unroll
+                    for (int k = GS * g; k < GS * g + GS; k += 2) {
+                        const f32x2 x = fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), af2, bm2);
+                        const f32x2 e = pack2(exp2_approx(lo2(x)), exp2_approx(hi2(x)));
+                        sum = add2(sum, e);
+                        v[k / 2] = pack_f16(lo2(e), hi2(e));
+                    }
+                    l = fmaf(lo2(sum) + hi2(sum), f[g].z, l);
+                }
+                tc::st32(ts, reinterpret_cast<uint32_t(&)[32]>(v[0]));
                 tc::wait_st();
                 tc::fence_before();
-                arrive(&bars->p_half[w]);
-                l += sum + weights(2) + weights(3);
-                store(2);
-                store(3);
-                tc::wait_st();
-                tc::fence_before();
-                arrive(&bars->p_full[w]);
+                arrive(&bars->p_full[w][half]);
             }
 
             // ---- the row's output -------------------------------------------------
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 }
             }
         }
-    } else if (warp > 8) {
+    } else if (warp > 9) {
         // ---- codes to fp16 ------------------------------------------------------
         regs_down<kRegsRest>();
         // Of K and of V: 16-code chunks per key in this CTA, keys a warp takes at a
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
         constexpr int ITERS = (GROUPS + kConvWarps - 1) / kConvWarps;
         constexpr int AHEAD = S::kRaw / 2;
         static_assert(kKeys / RPW[1] == GROUPS, "K and V items have one size");
-        const int cw = warp - 9;
+        const int cw = warp - 10;
         // A lane's key and chunk: 8 neighbouring lanes write 4 chunks of two
         // neighbouring rows, whose swizzled places fall on different banks.
         int kr[2], cc[2];
@@ -511,10 +513,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         regs_down<kRegsRest>();
-        if (warp == 8 && rank == 0 && steps > 0) {
+        const int w = warp - 8;
+        if (w < (two ? 2 : 1) && rank == 0 && steps > 0) {
             const bool lead = lane == 0;
             // ---- MMAs -----------------------------------------------------------
-            constexpr uint32_t kIS = f16_idesc(128 * CTAS, kKeys, false), kIO = f16_idesc(128 * CTAS, D, true);
+            constexpr uint32_t kIS = f16_idesc(128 * CTAS, kKeys / 2, false), kIO = f16_idesc(128 * CTAS, D, true);
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 const bool ok = tc::wait(bar, parity, p.wait_limit_ns);
                 tc::fence_after();
@@ -529,45 +532,43 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             };
             const uint32_t q_low = tc::desc_low_kmajor(sq), k_low = tc::desc_low_kmajor(skv);
             const uint32_t v_low = tc::desc_low_mnmajor(skv, S::kVAtom);
-            auto scores = [&](int w, int st) {
-                const uint32_t q = q_low + w * (S::kQ >> 4), k = k_low + st * (S::kStage >> 4);
+            // S of one half of a step's keys: K rows 64 half (of a pair 32 half in each CTA)
+            auto scores = [&](int st, int half) {
+                const uint32_t q = q_low + w * (S::kQ >> 4), k = k_low + (st * S::kStage + half * (S::kKAtom / 2) >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint64_t a = tc::desc(q + (ks >> 2) * (S::kQAtom >> 4) + (ks & 3) * 2);
                     const uint64_t b = tc::desc(k + (ks >> 2) * (S::kKAtom >> 4) + (ks & 3) * 2);
                     if constexpr (PAIR)
-                        tc::mma_f16_pair(tmem + 128 * w, a, b, kIS, ks > 0, lead);
+                        tc::mma_f16_pair(tmem + 128 * w + 64 * half, a, b, kIS, ks > 0, lead);
                     else
-                        tc::mma_f16(tmem + 128 * w, a, b, kIS, ks > 0, lead);
+                        tc::mma_f16(tmem + 128 * w + 64 * half, a, b, kIS, ks > 0, lead);
                 }
-                commit(&bars->s_full[w]);
             };
-            // the first or second half of a step's keys
-            auto values = [&](int w, int st, int j, int half) {
+            auto values = [&](int st, int j, int half) {
                 const uint32_t v = v_low + st * (S::kStage >> 4);
 #pragma unroll
-                for (int ks = 4 * half; ks < 4 * half + 4; ++ks) {
-                    const uint64_t b = tc::desc(v + ks * (2048 >> 4));
-                    const uint32_t a = tmem + 128 * w + 8 * ks, d = tmem + 256 + 128 * w;
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t b = tc::desc(v + half_key<PAIR>(half, 16 * ks) * (128 >> 4));
+                    const uint32_t a = tmem + 128 * w + 64 * half + 8 * ks, d = tmem + 256 + 128 * w;
                     if constexpr (PAIR)
-                        tc::mma_f16_ta_pair(d, a, b, kIO, j > 0 || ks > 0, lead);
+                        tc::mma_f16_ta_pair(d, a, b, kIO, j > 0 || half > 0 || ks > 0, lead);
                     else
-                        tc::mma_f16_ta(d, a, b, kIO, j > 0 || ks > 0, lead);
+                        tc::mma_f16_ta(d, a, b, kIO, j > 0 || half > 0 || ks > 0, lead);
                 }
             };
-            const int tiles = two ? 2 : 1;
             int next = 0, phase = 0; // the next item's stage
             auto advance = [&] {
                 if (++next == RING)
                     next = 0, phase ^= 1;
             };
-            bool fine = true;
-            for (int w = 0; w < tiles && fine; ++w)
-                fine = wait(&bars->q_full[w], 0);
-            fine = fine && wait(&bars->kv_full[0], 0);
+            bool fine = wait(&bars->q_full[w], 0) && wait(&bars->kv_full[0], 0);
             if (fine) {
-                for (int w = 0; w < tiles; ++w)
-                    scores(w, 0);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    scores(0, half);
+                    commit(&bars->s_full[w][half]);
+                }
                 commit(&bars->kv_empty[0]);
             }
             advance();
@@ -580,30 +581,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 fine = wait(&bars->kv_full[vs], phase); // and K before it
                 advance();
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (w >= tiles || !fine)
-                        break;
-                    fine = wait(&bars->p_half[w], j & 1);
+                for (int half = 0; half < 2; ++half) {
+                    fine = fine && wait(&bars->p_full[w][half], j & 1);
                     if (!fine)
                         break;
-                    values(w, vs, j, 0);
-                    fine = wait(&bars->p_full[w], j & 1);
-                    if (!fine)
-                        break;
-                    values(w, vs, j, 1);
-                    if (w == tiles - 1)
-                        commit(&bars->kv_empty[vs]);
-                    if (more) {
-                        scores(w, ks);
-                        if (w == tiles - 1)
-                            commit(&bars->kv_empty[ks]);
-                    }
+                    values(vs, j, half);
+                    if (more)
+                        scores(ks, half);
+                    commit(&bars->s_full[w][half]);
                 }
+                commit(&bars->kv_empty[vs]);
+                if (more)
+                    commit(&bars->kv_empty[ks]);
             }
-            for (int w = 0; w < 2; ++w)
-                commit(&bars->o_full[w]);
+            commit(&bars->o_full[w]);
             // every MMA has finished before the tensor memory goes
-            (void)tc::wait(&bars->o_full[0], 0, p.wait_limit_ns);
+            (void)tc::wait(&bars->o_full[w], 0, p.wait_limit_ns);
         }
     }
     if (failed)
@@ -622,10 +615,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
     }
 }
 
-template <int D, bool FP8, bool PAIR> cudaError_t launch_tiles(const KvAttendParams &p, cudaStream_t stream)
+template <int D, bool FP8, bool PAIR, bool COARSE> cudaError_t launch_tiles(const KvAttendParams &p, cudaStream_t stream)
 {
     using S = TileShape<D, PAIR>;
-    auto kern = kv_attend_tiles_kernel<D, FP8, PAIR>;
+    auto kern = kv_attend_tiles_kernel<D, FP8, PAIR, COARSE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
     if (e != cudaSuccess)
         return e;
@@ -645,15 +638,21 @@ template <int D, bool FP8, bool PAIR> cudaError_t launch_tiles(const KvAttendPar
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+
+template <int D, bool PAIR> cudaError_t launch_tiles(const KvAttendParams &p, cudaStream_t stream)
+{
+    if (p.cache.page >= 32)
+        return p.cache.fp8 ? launch_tiles<D, true, PAIR, true>(p, stream) : launch_tiles<D, false, PAIR, true>(p, stream);
+    return p.cache.fp8 ? launch_tiles<D, true, PAIR, false>(p, stream) : launch_tiles<D, false, PAIR, false>(p, stream);
+}
+
 } // namespace
 
 cudaError_t launch_kv_attend_tiles(const KvAttendParams &p, cudaStream_t stream)
 {
     if (p.cache.d == 64)
-        return p.cache.fp8 ? launch_tiles<64, true, false>(p, stream) : launch_tiles<64, false, false>(p, stream);
-    if (kv_attend_pairs(p))
-        return p.cache.fp8 ? launch_tiles<128, true, true>(p, stream) : launch_tiles<128, false, true>(p, stream);
-    return p.cache.fp8 ? launch_tiles<128, true, false>(p, stream) : launch_tiles<128, false, false>(p, stream);
+        return launch_tiles<64, false>(p, stream);
+    return kv_attend_pairs(p) ? launch_tiles<128, true>(p, stream) : launch_tiles<128, false>(p, stream);
 }
 
 } // namespace ss24
