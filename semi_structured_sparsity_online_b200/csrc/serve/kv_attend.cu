@@ -470,9 +470,20 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) kv_attend_jo
     const int32_t heads = p.cache.kv_heads * p.group;
     const int64_t flat = blockIdx.x;
     const int32_t token = blockIdx.x / heads, head = blockIdx.x - token * heads;
+    __shared__ int32_t owned;
+    if (tid == 0)
+        owned = 0;
     grid_dependency_wait();
-    // tokens outside starts[0] .. starts[seqs] belong to no sequence
-    if (token < p.batch.starts[0] || token >= p.batch.starts[p.batch.seqs])
+    __syncthreads();
+    // the token's sequence; tokens of none, or of one that breaks a bound, have no parts
+    for (int64_t s = tid; s < p.batch.seqs; s += threads) {
+        int32_t first, count, len;
+        if (token >= __ldg(p.batch.starts + s) && token < __ldg(p.batch.starts + s + 1) &&
+            kv_sequence(p.batch, s, p.err, &first, &count, &len))
+            owned = 1;
+    }
+    __syncthreads();
+    if (!owned)
         return;
     const float *lse = p.part_lse + flat * p.splits;
     float top = -INFINITY;

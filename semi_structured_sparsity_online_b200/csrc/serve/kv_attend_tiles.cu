@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             row_before = row;
             row = on ? (ph << p.cache.log2_page) + (key & (p.cache.page - 1)) : -1;
             if (cw == 0) {
-                s_k = __ldg(p.cache.scales[0] + ph);
+                s_k = on ? __ldg(p.cache.scales[0] + ph) : 0.0f;
                 s_v = on ? __ldg(p.cache.scales[1] + ph) : -1.0f;
             }
             id = load_id(j + 1);
@@ -443,7 +443,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                     const bool on = first_row >= 0 && begin + j * kKeys + at < end;
                     if (group(it) < GROUPS)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_at(j, kv) + group(it) * 512),
-                                     "l"(codes + static_cast<int64_t>(on ? first_row + (at & 15) : 0) * D),
+                                     "l"(on ? codes + static_cast<int64_t>(first_row + (at & 15)) * D
+                                            : static_cast<const uint8_t *>(p.q.x)), // nothing is read there
                                      "r"(on ? 16 : 0));
                 }
             }

@@ -524,6 +524,9 @@ def gemm_int8(a, b, dtype=torch.bfloat16, y=None, ws=None, stream=None):
     tokens and [n, k] channels (``values`` int8, ``scales`` float32 [rows, 1]).
     Returns [m, n] in `dtype` (bfloat16 or float32), or fills `y` (its dtype;
     the columns contiguous, any row stride)."""
+    if stream is not None and y is None and stream != torch.cuda.current_stream(stream.device):
+        with torch.cuda.stream(stream):  # what is allocated here belongs to the stream that uses it
+            return gemm_int8(a, b, dtype, None, ws)
     av, sa = _int8_rows(a, "a")
     bv, sb = _int8_rows(b, "b")
     (m, k), (n, kb) = av.shape, bv.shape

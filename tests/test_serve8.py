@@ -102,6 +102,17 @@ def test_gemm_int8_takes_the_quantizers_rows(ss):
     assert float((y - x.float() @ w.float().T).norm() / (x.float() @ w.float().T).norm()) < 0.02
 
 
+def test_gemm_int8_allocates_for_the_stream_it_runs_on(ss):
+    a, b = int8_operand(70, 4096, 12), int8_operand(4096, 4096, 13)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    ys = [ss.gemm_int8(a, b, dtype=torch.float32, stream=s) for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(s)
+    for y in ys:
+        check_product(y, a, b)
+
+
 def test_gemm_int8_on_another_stream_and_replayed(ss):
     a, b = int8_operand(20, 512, 10), int8_operand(300, 512, 11)
     ws = ss.Workspace()
@@ -391,7 +402,8 @@ def test_attention_single_tokens(ss, fmt, d, page, heads, group, tight):
 
 
 @pytest.mark.parametrize("fmt", ["int", "fp8"])
-@pytest.mark.parametrize("d,page,heads,group", [(128, 64, 2, 4), (64, 16, 1, 7), (64, 128, 2, 1), (128, 32, 1, 8)])
+@pytest.mark.parametrize("d,page,heads,group", [(128, 64, 2, 4), (64, 16, 1, 7), (64, 128, 2, 1), (128, 32, 1, 8),
+                                                (128, 16, 1, 3), (64, 32, 1, 2)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_attention_many_tokens(ss, fmt, d, page, heads, group, causal):
     """Prompts and pieces of them, ragged; more new tokens than keys leave rows empty."""
@@ -399,6 +411,36 @@ def test_attention_many_tokens(ss, fmt, d, page, heads, group, causal):
     news = [1, 5, 130, 100, 33, 1, 9, 4, 257, 70]
     layer = Layer(ss, fmt, d, page, heads, max(lens), len(lens), seed=d * page).fill(lens)
     attend(ss, layer, lens, news, group, causal, max_new=max(news), max_len=max(lens))
+
+
+@pytest.mark.parametrize("fmt", ["int", "fp8"])
+@pytest.mark.parametrize("d,page", [(128, 16), (128, 64), (64, 16), (64, 128)])
+@pytest.mark.parametrize("rows", [17, 127, 128, 129, 255, 256, 257, 511, 512, 513, 640])
+def test_attention_row_counts_around_tiles(ss, fmt, d, page, rows):
+    """One KV head, one query head: as many rows as new tokens, next to a single token, over a cached prefix."""
+    lens, news = [rows + 45, 7, rows], [rows, 1, rows - 1]
+    layer = Layer(ss, fmt, d, page, 1, max(lens), 3, seed=rows).fill(lens)
+    attend(ss, layer, lens, news, 1, True, max_new=rows, max_len=max(lens))
+
+
+@pytest.mark.parametrize("seqs", [257, 600])
+def test_attention_more_sequences_than_threads(ss, seqs):
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(0, 40, seqs).tolist()
+    layer = Layer(ss, "int", 64, 16, 1, 40, seqs, seed=19).fill(lens)
+    attend(ss, layer, lens, [1] * seqs, 2, True, max_new=1, max_len=40)
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_attention_without_keys_or_pages(ss, new):
+    """No sequence has a key; a cache without pages."""
+    for pages in (3, 0):
+        cache = ss.kv_cache(pages, 2, 64, page=16)
+        q = torch.randn(2 * new, 4, 64, generator=gen(1), device="cuda").bfloat16()
+        for width in (1, 0):
+            table = torch.full((2, width), 99, dtype=torch.int32, device="cuda")
+            out, lse = ss.kv_attention(q, cache, table, i32([0, new, 2 * new]), i32([0, 0]), lse=True)
+            assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
 
 @pytest.mark.parametrize("fmt,d,group,new", [("int", 128, 4, 1), ("fp8", 64, 8, 1), ("fp8", 128, 4, 40), ("int", 64, 1, 17)])
@@ -464,6 +506,51 @@ def test_attention_records_bad_pages_and_bounds(ss, new):
         assert torch.equal(out[new:], good[new:])  # the other sequence
     # a page that counts as no keys: as if those 16 keys were masked
     assert bool(torch.isfinite(out[new:].float()).all())
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_in_parts_leaves_out_a_sequence_that_breaks_a_bound(ss, new):
+    """Where the key axis is split, the rows of a bad sequence are left as they were, too."""
+    lens = [6000, 5000]
+    layer = Layer(ss, "int", 64, 64, 1, 6000, 2, seed=20).fill(lens)
+    q = torch.randn(2 * new + 3, 2, 64, generator=gen(2), device="cuda").bfloat16()
+    table, starts = layer.table(lens), i32([0, new, 2 * new])
+    good, good_lse = ss.kv_attention(q, layer.cache, table, starts, i32(lens), max_new=new, max_len=6000, lse=True)
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:2], 5.0, device="cuda")
+    ws = ss.Workspace()
+    ss.kv_attention(q, layer.cache, table, starts, i32([6001, 5000]), max_new=new, max_len=6000, out=out, lse=lse, ws=ws)
+    assert ws.error() == 17
+    assert bool((out[:new] == 5.0).all()) and bool((lse[:new] == 5.0).all())
+    assert torch.equal(out[new:2 * new], good[new:2 * new]) and torch.equal(lse[new:2 * new], good_lse[new:2 * new])
+    assert bool((out[2 * new:] == 5.0).all()) and bool((lse[2 * new:] == 5.0).all())
+
+
+@pytest.mark.parametrize("fmt", ["int", "fp8"])
+def test_a_cache_beyond_4_gib(ss, fmt):
+    """Pages whose codes lie past 2^32 bytes: written, read by few rows, by many and in parts."""
+    page, heads, d = 128, 8, 128
+    pages = (1 << 32) // (page * heads * d) + 40
+    dt = torch.int8 if fmt == "int" else torch.uint8
+    cache = {n: torch.empty(pages, heads, page, d, dtype=dt, device="cuda") for n in ("k", "v")}
+    cache.update({n: torch.zeros(pages, heads, device="cuda") for n in ("k_scales", "v_scales")})
+    cache.update(page=page, fmt=fmt)
+    small = ss.kv_cache(24, heads, d, page=page, fmt=fmt)
+    length = 24 * page - 5
+    x = torch.randn(length, 2 * heads, d, generator=gen(3), device="cuda").bfloat16()
+    where = (i32([0, length]), i32([length]))
+    far = torch.arange(pages - 24, pages, dtype=torch.int32, device="cuda").view(1, 24)
+    near = torch.arange(24, dtype=torch.int32, device="cuda").view(1, 24)
+    ss.kv_append(cache, x[:, :heads], x[:, heads:], far, *where)
+    ss.kv_append(small, x[:, :heads], x[:, heads:], near, *where)
+    for n in ("k_scales", "v_scales"):
+        assert torch.equal(cache[n][pages - 24:], small[n])
+    for new in (1, 20, 300):
+        q = torch.randn(new, 2 * heads, d, generator=gen(4), device="cuda").bfloat16()
+        st = i32([0, new])
+        a = ss.kv_attention(q, cache, far, st, where[1], max_len=length, lse=True)
+        b = ss.kv_attention(q, small, near, st, where[1], max_len=length, lse=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 @pytest.mark.parametrize("new", [1, 20])
