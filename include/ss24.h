@@ -109,8 +109,9 @@
  * are valid once the stream is synchronized. Kernels never trap: an internal
  * wait that exceeds about two seconds records a nonzero code in the
  * workspace (read with ss24_workspace_error) and the kernel returns; its
- * outputs and energies are then incomplete. The only kernels with such waits
- * are those of the strided axis (axis 0), which wait on their tile copies.
+ * outputs and energies are then incomplete. The kernels with such waits are
+ * those of the strided axis (axis 0), which wait on their tile copies, the
+ * sparse product and the serving operators.
  *
  * Test hook. When the environment variable SS24_TEST_SKIP_TILE holds a
  * number t >= 0 at the time of a call, the first CTA of that call's

@@ -14,13 +14,13 @@
 //             warps' of its scheduler, as long as it runs: hence two warps.
 //   10-15     codes of K and V from the pages to fp16 in shared memory, a ring
 //             of stages in the 128-byte swizzle that the MMA reads
+//
 // PAIR: two CTAs of a cluster work on twice the rows with cta_group::2 MMAs.
 // Each brings half of every B operand (64 keys of K, 64 of the 128 elements of
-// V) and its own rows: a step's shared-memory traffic per SM, which bounds the
-// single form (192 KB of MMA reads and 128 KB of conversion, 2500 cycles
-// against 2048 of MMA), halves on the side of the keys, and so does the
-// conversion. The even CTA's lane issues for both; barriers that it waits on
-// are arrived on by both.
+// V) and its own rows: conversion and the shared-memory reads of K and V halve
+// per SM. (Per step of 128 keys the single form converts 32 KB of codes and
+// moves 320 KB through shared memory, 2500 cycles beside 2048 of MMA.) The even
+// CTA's lanes issue for both; barriers that they wait on are arrived on by both.
 //
 // A step's S is handled in two halves of 64 keys with barriers of their own:
 // while a row's thread works on one half, the tensor cores multiply the weights
@@ -29,6 +29,11 @@
 // In whole steps a row tile's softmax and its MMAs waited for each other, 2400
 // and 1400 cycles of a step of 4100. The output is rescaled when a row's bound M
 // moves by more than 2^8, which waits for the other half's products first.
+//
+// Measured: a prompt of 8192 tokens, 32 heads of 128 on 8 KV heads, INT8, pages of
+// 64: 550 us, 1.0 PFLOP/s (0.61 of the measured peak), tensor pipe 48% and
+// special-function unit 48% active. 4 x up to 509 tokens over up to 4000 keys, 28
+// heads of 64 on 4, E4M3, pages of 16: 82 us, special functions 52%.
 #include "kv_attend.cuh"
 #include "tcgen05.cuh"
 
