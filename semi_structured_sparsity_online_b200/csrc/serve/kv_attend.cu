@@ -72,17 +72,18 @@ __device__ __forceinline__ uint2 lds8(uint32_t addr)
 }
 
 constexpr int kRowWarps = 8;               // they take a part's 16-key groups in turn
+constexpr int kRows = 8;                   // of a tile: the MMA's N
 
-template <int D, int NT> struct RowShape {
-    static constexpr int kRing = (D == 128 ? 3 : 6) * (NT == 1 ? 1 : 2);
+template <int D> struct RowShape {
+    static constexpr int kRing = D == 128 ? 3 : 6;
     static constexpr uint32_t kBox = 16 * D;      // 16 keys of K or of V
     static constexpr uint32_t kGroup = 2 * kBox;
-    static constexpr int kPerSm = NT == 1 ? 2 : 1;
+    static constexpr int kPerSm = 2;
     // afterwards the boxes hold the warps' sums [warp][row][D + 4]
-    static constexpr uint32_t kSums = kRowWarps * 8 * NT * (D + 4) * 4;
+    static constexpr uint32_t kSums = kRowWarps * kRows * (D + 4) * 4;
     static constexpr uint32_t kTiles =
         kRowWarps * kRing * kGroup > kSums ? kRowWarps * kRing * kGroup : kSums;
-    static constexpr size_t kSmem = 1024 + kTiles + 2 * kRowWarps * 8 * NT * 4 + kRowWarps * kRing * 8;
+    static constexpr size_t kSmem = 1024 + kTiles + 2 * kRowWarps * kRows * 4 + kRowWarps * kRing * 8;
 };
 
 // 16-byte chunk c of row r in a swizzled box.
@@ -117,14 +118,13 @@ __device__ __forceinline__ int32_t longest_first(const KvBatch &b, uint32_t rank
     return s;
 }
 
-// NT: n tiles of 8 rows.
-template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
     kv_attend_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                           const KvAttendParams p)
 {
-    using S = RowShape<D, NT>;
-    constexpr int ROWS = 8 * NT, MT = D / 16, WARPS = kRowWarps, RING = S::kRing;
+    using S = RowShape<D>;
+    constexpr int ROWS = kRows, MT = D / 16, WARPS = kRowWarps, RING = S::kRing;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     uint8_t *gen = smem_raw + (base - smem_u32(smem_raw));
@@ -219,17 +219,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
     }
     load_scales();
 
-    // q: n tile t, row g: the 4 values of d that step ks of K's lane layout names
-    uint32_t qf[NT][MT][2];
-    float fac[NT][2];
-    int32_t limit[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    // q of row g: the 4 values of d that step ks of K's lane layout names
+    uint32_t qf[MT][2];
+    float fac[2];
+    int32_t limit[2];
+    {
         float v[MT][4];
         float amax = 0.0f;
-        const int r = 8 * t + g;
-        const bool on = r < live;
-        const RowAt a = row_at(p, row0 + (on ? r : 0), h, first, count, len);
+        const bool on = g < live;
+        const RowAt a = row_at(p, row0 + (on ? g : 0), h, first, count, len);
         const __nv_bfloat16 *src =
             static_cast<const __nv_bfloat16 *>(p.q.x) + a.token * p.q.token_ld + a.head * p.q.head_ld;
 #pragma unroll
@@ -252,25 +250,22 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
         const float down = exp2_int(-e);
 #pragma unroll
         for (int ks = 0; ks < MT; ++ks) {
-            qf[t][ks][0] = pack_f16(v[ks][0] * down, v[ks][1] * down);
-            qf[t][ks][1] = pack_f16(v[ks][2] * down, v[ks][3] * down);
+            qf[ks][0] = pack_f16(v[ks][0] * down, v[ks][1] * down);
+            qf[ks][1] = pack_f16(v[ks][2] * down, v[ks][3] * down);
         }
         const float f = p.scale_log2 * exp2_int(e);
         // the accumulators' rows of this lane: 2q, 2q + 1
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            fac[t][i] = __shfl_sync(kFull, f, (2 * q + i) * 4);
-            const int rr = 8 * t + 2 * q + i;
-            limit[t][i] = rr < live ? row_at(p, row0 + rr, h, first, count, len).limit : 0;
+            fac[i] = __shfl_sync(kFull, f, (2 * q + i) * 4);
+            const int r = 2 * q + i;
+            limit[i] = r < live ? row_at(p, row0 + r, h, first, count, len).limit : 0;
         }
     }
     const int32_t low = row_at(p, row0, h, first, count, len).limit; // the least any row sees
 
-    float o[NT][MT][4] = {};
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-        m[t][0] = m[t][1] = -1e30f, l[t][0] = l[t][1] = 0.0f;
+    float o[MT][4] = {};
+    float m[2] = {-1e30f, -1e30f}, l[2] = {0.0f, 0.0f};
 
     int slot = 0, phase = 0;
     for (int i = 0; i < groups; ++i) {
@@ -292,7 +287,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
         const uint32_t k_at = ring + slot * S::kGroup, v_at = k_at + S::kBox;
         if (page >= 0) {
             // two chains of products, even and odd steps
-            float sc[NT][4] = {}, sd[NT][4] = {};
+            float sc[4] = {}, sd[4] = {};
             uint4 wa, wb;
 #pragma unroll
             for (int ks = 0; ks < MT; ++ks) {
@@ -305,57 +300,48 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
                 uint32_t a0, a1, a2, a3;
                 codes4_to_f16<FP8>(a, a0, a2);
                 codes4_to_f16<FP8>(c, a1, a3);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    mma_f16((ks & 1) ? sd[t] : sc[t], a0, a1, a2, a3, qf[t][ks][0], qf[t][ks][1]);
+                mma_f16((ks & 1) ? sd : sc, a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
             }
-            // sc[t]: (key g, rows 2q, 2q + 1), (key g + 8, the same rows)
+            // sc: (key g, rows 2q, 2q + 1), (key g + 8, the same rows)
             const bool edge = key + 16 > ke || key + 16 > low;
             bool above = false;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sc[t][i] = fmaf(sc[t][i] + sd[t][i], ks_i * fac[t][i & 1], lsv);
-                    if (edge) {
-                        const int32_t j = key + g + 8 * (i >> 1);
-                        if (j >= limit[t][i & 1] || j >= ke)
-                            sc[t][i] = -INFINITY;
-                    }
-                    above |= sc[t][i] > m[t][i & 1] + 8.0f;
+            for (int i = 0; i < 4; ++i) {
+                sc[i] = fmaf(sc[i] + sd[i], ks_i * fac[i & 1], lsv);
+                if (edge) {
+                    const int32_t j = key + g + 8 * (i >> 1);
+                    if (j >= limit[i & 1] || j >= ke)
+                        sc[i] = -INFINITY;
                 }
+                above |= sc[i] > m[i & 1] + 8.0f;
+            }
             if (__any_sync(kFull, above)) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int i = 0; i < 2; ++i) {
+                    float x = fmaxf(sc[i], sc[i + 2]);
+                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+                    x = fmaxf(x, m[i]);
+                    const float f = exp2_approx(m[i] - x);
+                    m[i] = x;
+                    l[i] *= f;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float x = fmaxf(sc[t][i], sc[t][i + 2]);
-                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-                        x = fmaxf(x, m[t][i]);
-                        const float f = exp2_approx(m[t][i] - x);
-                        m[t][i] = x;
-                        l[t][i] *= f;
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            o[t][mt][i] *= f;
-                            o[t][mt][i + 2] *= f;
-                        }
+                    for (int mt = 0; mt < MT; ++mt) {
+                        o[mt][i] *= f;
+                        o[mt][i + 2] *= f;
                     }
+                }
             }
-            uint32_t pf[NT][2];
+            uint32_t pf[2];
+            float w[4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = exp2_approx(sc[t][i] - m[t][i & 1]);
-                l[t][0] = fmaf(w[0] + w[2], inv, l[t][0]);
-                l[t][1] = fmaf(w[1] + w[3], inv, l[t][1]);
-                pf[t][0] = transpose8x8(pack_f16(w[0], w[1]));
-                pf[t][1] = transpose8x8(pack_f16(w[2], w[3]));
-            }
+            for (int i = 0; i < 4; ++i)
+                w[i] = exp2_approx(sc[i] - m[i & 1]);
+            l[0] = fmaf(w[0] + w[2], inv, l[0]);
+            l[1] = fmaf(w[1] + w[3], inv, l[1]);
+            pf[0] = transpose8x8(pack_f16(w[0], w[1]));
+            pf[1] = transpose8x8(pack_f16(w[2], w[3]));
             // of V, lane (g, q) takes the D / 8 bytes at g D / 8 of keys 2q, 2q + 1, 2q + 8, 2q + 9
             uint32_t v[4][D / 32];
 #pragma unroll
@@ -384,11 +370,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
                 uint32_t lo[4], hi[4];
                 pairs4_to_f16<FP8>(v[0][w], v[1][w], lo);
                 pairs4_to_f16<FP8>(v[2][w], v[3][w], hi);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma_f16(o[t][2 * w], lo[0], lo[1], hi[0], hi[1], pf[t][0], pf[t][1]);
-                    mma_f16(o[t][2 * w + 1], lo[2], lo[3], hi[2], hi[3], pf[t][0], pf[t][1]);
-                }
+                mma_f16(o[2 * w], lo[0], lo[1], hi[0], hi[1], pf[0], pf[1]);
+                mma_f16(o[2 * w + 1], lo[2], lo[3], hi[2], hi[3], pf[0], pf[1]);
             }
         }
         // every lane has read the slot: the group RING on takes it
@@ -407,20 +390,18 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D, NT>::kPerSm)
     __syncthreads();
     // the warps' sums joined
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(kFull, l[i], 4);
+        l[i] += __shfl_xor_sync(kFull, l[i], 8);
+        l[i] += __shfl_xor_sync(kFull, l[i], 16);
+        const int r = 2 * q + i;
+        if (g == 0)
+            sm_m[warp][r] = m[i], sm_l[warp][r] = l[i];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[t][i] += __shfl_xor_sync(kFull, l[t][i], 4);
-            l[t][i] += __shfl_xor_sync(kFull, l[t][i], 8);
-            l[t][i] += __shfl_xor_sync(kFull, l[t][i], 16);
-            const int r = 8 * t + 2 * q + i;
-            if (g == 0)
-                sm_m[warp][r] = m[t][i], sm_l[warp][r] = l[t][i];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                *reinterpret_cast<float2 *>(&sm_o[warp][r][g * (D / 8) + 2 * mt]) =
-                    make_float2(o[t][mt][i], o[t][mt][i + 2]);
-        }
+        for (int mt = 0; mt < MT; ++mt)
+            *reinterpret_cast<float2 *>(&sm_o[warp][r][g * (D / 8) + 2 * mt]) =
+                make_float2(o[mt][i], o[mt][i + 2]);
+    }
     if (failed)
         atomicCAS(p.err, 0, kErrAttendWait);
     __syncthreads();
@@ -571,12 +552,12 @@ cudaError_t launch(K kern, int64_t grid, int threads, size_t smem, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Up to 16 rows per (sequence, KV head) go to the kernel above, in tiles of 8
-// or 16; more rows to the tensor-memory kernel in tiles of 256.
-bool narrow(const KvAttendParams &p) { return p.batch.max_new * p.group <= 8; }
-bool wide(const KvAttendParams &p) { return p.batch.max_new * p.group > 16; }
+// Up to 32 rows per (sequence, KV head) go to the kernel above, more to the
+// tensor-memory kernel in tiles of 256 (16 sequences of up to 8192 keys, 8 KV heads
+// of 128: 32 rows 86 and 145 us, 96 rows 151 and 137).
+bool wide(const KvAttendParams &p) { return p.batch.max_new * p.group > 32; }
 
-template <int D, bool FP8, int NT> cudaError_t launch_rows(const KvAttendParams &p, cudaStream_t stream)
+template <int D, bool FP8> cudaError_t launch_rows(const KvAttendParams &p, cudaStream_t stream)
 {
     CUtensorMap mk, mv;
     // a cache without pages: maps that no copy uses
@@ -585,13 +566,8 @@ template <int D, bool FP8, int NT> cudaError_t launch_rows(const KvAttendParams 
     if (!tensor_map_bytes(&mk, none ? p.q.x : p.cache.codes[0], rows, D, D, 16) ||
         !tensor_map_bytes(&mv, none ? p.q.x : p.cache.codes[1], rows, D, D, 16))
         return cudaErrorInvalidValue;
-    return launch(kv_attend_rows_kernel<D, FP8, NT>, p.batch.seqs * p.cache.kv_heads * p.row_tiles * p.splits,
-                  kRowWarps * 32, RowShape<D, NT>::kSmem, stream, mk, mv, p);
-}
-
-template <int D, bool FP8> cudaError_t launch_rows(const KvAttendParams &p, cudaStream_t stream)
-{
-    return narrow(p) ? launch_rows<D, FP8, 1>(p, stream) : launch_rows<D, FP8, 2>(p, stream);
+    return launch(kv_attend_rows_kernel<D, FP8>, p.batch.seqs * p.cache.kv_heads * p.row_tiles * p.splits,
+                  kRowWarps * 32, RowShape<D>::kSmem, stream, mk, mv, p);
 }
 
 } // namespace
@@ -601,7 +577,7 @@ void kv_attend_plan(KvAttendParams *p)
     const int64_t rows = p->batch.max_new * p->group;
     const int64_t len = p->batch.max_len > 0 ? p->batch.max_len : 1;
     const int pair = wide(*p) && kv_attend_pairs(*p) ? 2 : 1;
-    const int64_t tile = wide(*p) ? pair * kTileRows : narrow(*p) ? 8 : 16;
+    const int64_t tile = wide(*p) ? pair * kTileRows : kRows;
     p->row_tiles = static_cast<int32_t>(ceil_div(rows, tile));
     const int64_t ctas = p->batch.seqs * p->cache.kv_heads * p->row_tiles;
     // Parts of the key axis: as many CTAs as run at once and no more, of 512 keys
@@ -609,8 +585,14 @@ void kv_attend_plan(KvAttendParams *p)
     // each: 53 us in one wave of 296, 58 in two, 68 in four). Smaller parts save
     // little on the device and cost the join's launch (500 keys: 7.4 us in one
     // part, 7.8 in two; 1000 keys: 9.4 in two, 8.2 in four).
-    const int64_t step = 128;
-    int64_t splits = ctas > 0 ? 148 * (wide(*p) ? 1 : 2) / (pair * ctas) : 1;
+    // Where that leaves parts of more than 4096 keys, sequences of unequal lengths
+    // hold up the wave: two waves of shorter parts (16 sequences of 1024 to 8192
+    // keys, 8 heads, 16 rows each: 54 us instead of 86; all of 8192 keys: 99
+    // instead of 91). A single sequence stays with one.
+    const int64_t step = 128, slots = 148 * (wide(*p) ? 1 : RowShape<128>::kPerSm);
+    int64_t splits = ctas > 0 ? slots / (pair * ctas) : 1;
+    if (!wide(*p) && ctas > 0 && p->batch.seqs > 1 && (splits == 0 || len / splits > 4096))
+        splits = 2 * slots / ctas;
     const int64_t most = ceil_div(len, 4 * step);
     splits = splits > most ? most : splits;
     splits = splits < 1 ? 1 : splits > kMaxParts ? kMaxParts : splits;
