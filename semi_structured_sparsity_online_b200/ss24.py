@@ -505,7 +505,13 @@ def _enqueue(index, stream, name, *args):
 
 
 def _workspace(ws, t):
-    return ws if ws is not None else default_workspace(t.device)
+    if ws is not None:
+        return ws
+    ws = _default_ws.get(t.device)
+    if ws is None:
+        with torch.cuda.device(t.device):
+            ws = default_workspace(t.device)
+    return ws
 
 
 def _int8_rows(d, name):

@@ -415,7 +415,7 @@ def test_attention_many_tokens(ss, fmt, d, page, heads, group, causal):
 
 @pytest.mark.parametrize("fmt", ["int", "fp8"])
 @pytest.mark.parametrize("d,page", [(128, 16), (128, 64), (64, 16), (64, 128)])
-@pytest.mark.parametrize("rows", [17, 127, 128, 129, 255, 256, 257, 511, 512, 513, 640])
+@pytest.mark.parametrize("rows", [9, 16, 17, 25, 32, 33, 127, 128, 129, 255, 256, 257, 511, 512, 513, 640])
 def test_attention_row_counts_around_tiles(ss, fmt, d, page, rows):
     """One KV head, one query head: as many rows as new tokens, next to a single token, over a cached prefix."""
     lens, news = [rows + 45, 7, rows], [rows, 1, rows - 1]
@@ -431,7 +431,21 @@ def test_attention_more_sequences_than_threads(ss, seqs):
     attend(ss, layer, lens, [1] * seqs, 2, True, max_new=1, max_len=40)
 
 
-@pytest.mark.parametrize("new", [1, 20])
+@pytest.mark.parametrize("new", [1, 50])
+def test_a_slice_of_a_wider_page_table(ss, new):
+    lens = [90, 120]
+    layer = Layer(ss, "int", 64, 16, 1, 128, 2, seed=21).fill(lens)
+    q = torch.randn(2 * new, 2, 64, generator=gen(1), device="cuda").bfloat16()
+    starts, table = i32([0, new, 2 * new]), layer.table(lens)
+    wide = torch.full((2, 3 * table.shape[1]), 1 << 30, dtype=torch.int32, device="cuda")
+    part = wide[:, 5:5 + table.shape[1]]
+    part.copy_(table)
+    a = ss.kv_attention(q, layer.cache, table, starts, i32(lens))
+    b = ss.kv_attention(q, layer.cache, part, starts, i32(lens))
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("new", [1, 20, 40])
 def test_attention_without_keys_or_pages(ss, new):
     """No sequence has a key; a cache without pages."""
     for pages in (3, 0):
