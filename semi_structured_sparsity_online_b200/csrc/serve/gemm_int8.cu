@@ -190,10 +190,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int64_t own = t0 + 32 * w + lane;
             s[32 * w + lane] = own < p.m ? __ldg(p.a_scale + own) : 0.0f;
             named_barrier_sync(1 + half, 128);
-            if (!tc::wait(&bars->acc_full[a], (n >> 1) & 1, p.wait_limit_ns)) {
-                failed = true;
-                break;
-            }
+            // a warp that gave up still meets the others at the barrier above
+            failed = failed || !tc::wait_warp(&bars->acc_full[a], (n >> 1) & 1, p.wait_limit_ns);
+            if (failed)
+                continue;
             tc::fence_after();
             const int64_t room = p.m - t0;
             const int cols = static_cast<int>(room < 0 ? 0 : room < 128 ? room : 128);

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
         for (int i = 0; i < RING; ++i)
             mbar_init(&full[i], 1);
         fence_barrier_init();
+        tc::fence_proxy(); // the copies overwrite longest_first's room
     }
     __syncwarp();
     bool failed = false;
@@ -267,8 +268,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
     float o[MT][4] = {};
     float m[2] = {-1e30f, -1e30f}, l[2] = {0.0f, 0.0f};
 
-    int slot = 0, phase = 0;
-    for (int i = 0; i < groups; ++i) {
+    int slot = 0, phase = 0, i = 0;
+    for (; i < groups; ++i) {
         if (i > 0 && (i & 31) == 0) {
             id = id_next;
             if (i + lane < groups && (id < 0 || id >= p.cache.pages))
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
         const int32_t page = __shfl_sync(kFull, id, i & 31);
         const float ks_i = __shfl_sync(kFull, s_k, i & 31), lsv = __shfl_sync(kFull, s_v, i & 31),
                     inv = __shfl_sync(kFull, s_inv, i & 31);
-        if (!tc::wait(&full[slot], phase, p.wait_limit_ns)) {
+        if (!tc::wait_warp(&full[slot], phase, p.wait_limit_ns)) {
             failed = true;
             break;
         }
@@ -384,8 +385,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
     }
     // a wait that ran out: the copies on their way land before the CTA exits
     if (failed)
-        for (int i = 0; i < RING; ++i)
-            (void)tc::wait(&full[i], 0, p.wait_limit_ns / 8);
+        for (int n = i + RING; i < n && i < groups; ++i) {
+            (void)tc::wait(&full[slot], phase, p.wait_limit_ns / 8);
+            if (++slot == RING)
+                slot = 0, phase ^= 1;
+        }
     // every warp is through with the boxes before they take the sums
     __syncthreads();
     // the warps' sums joined

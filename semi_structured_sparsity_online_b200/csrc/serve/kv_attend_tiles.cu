@@ -238,10 +238,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             float m = -1e30f, l = 0.0f;
             for (int i = 0; i < 2 * steps; ++i) {
                 const int j = i >> 1, half = i & 1;
-                if (!tc::wait(&bars->s_full[w][half], j & 1, p.wait_limit_ns)) {
-                    failed = true;
-                    break;
-                }
+                // a lane that gives up says so in the vote below
+                const bool late = !tc::wait(&bars->s_full[w][half], j & 1, p.wait_limit_ns);
                 tc::fence_after();
                 const uint32_t ts = ts0 + 64 * half; // S, and the weights in its first half
                 const int32_t key0 = static_cast<int32_t>(kb) + j * kKeys;
@@ -277,14 +275,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                     x = max3(__float_as_uint(x), y[GS - 2], y[GS - 1]);
                     mx = fmaxf(mx, fmaf(fmaxf(x, z), f[g].x, f[g].y));
                 }
-                if (__any_sync(kFull, mx > m + 8.0f)) {
+                if (__any_sync(kFull, late || mx > m + 8.0f)) {
+                    if (__any_sync(kFull, late)) {
+                        failed = true;
+                        break;
+                    }
                     const float mn = fmaxf(m, mx), scale = exp2_approx(m - mn);
                     m = mn;
                     l *= scale;
                     if (i > 0) {
                         // the half before: its products are done when the S behind them is (or,
                         // in the last step, when the barrier that stands for it says so)
-                        if (!tc::wait(&bars->s_full[w][half ^ 1], (j + half) & 1, p.wait_limit_ns)) {
+                        if (!tc::wait_warp(&bars->s_full[w][half ^ 1], (j + half) & 1, p.wait_limit_ns)) {
                             failed = true;
                             break;
                         }
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             }
 
             // ---- the row's output -------------------------------------------------
-            if (!failed && steps > 0 && !tc::wait(&bars->o_full[w], 0, p.wait_limit_ns))
+            if (!failed && steps > 0 && !tc::wait_warp(&bars->o_full[w], 0, p.wait_limit_ns))
                 failed = true;
             tc::fence_after();
             const bool any = steps > 0 && l > 0.0f;
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 const int j = i - kv;
                 if (j < 0 || j >= steps)
                     continue;
-                if (!tc::wait(&bars->kv_empty[st], phase, p.wait_limit_ns)) {
+                if (!tc::wait_warp(&bars->kv_empty[st], phase, p.wait_limit_ns)) {
                     failed = true;
                     break;
                 }

@@ -28,6 +28,13 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint64_t li
     }
 }
 
+// The same by a whole warp, with one answer for all lanes: one that gave up by
+// itself would leave the others in the next vote or shuffle.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+    return __all_sync(kFull, wait(bar, parity, limit_ns));
+}
+
 // The warp's number, and a value that is the same in all its lanes, in a form
 // the compiler takes as uniform.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
