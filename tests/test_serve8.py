@@ -465,6 +465,15 @@ def test_attention_long_context(ss, fmt, d, group, new):
     attend(ss, layer, lens, news, group, True, max_new=new, max_len=max(lens))
 
 
+@pytest.mark.parametrize("fmt,d,heads,group", [("int", 128, 3, 7), ("fp8", 64, 1, 20), ("int", 64, 5, 4)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_chunks_in_parts(ss, fmt, d, heads, group, causal):
+    """Thousands of rows and a split key axis; a sequence shorter than a part, one with rows that see no key."""
+    lens, news = [2500, 130, 90], [151, 130, 100]
+    layer = Layer(ss, fmt, d, 32, heads, max(lens), 3, seed=d + heads).fill(lens)
+    attend(ss, layer, lens, news, group, causal, max_new=max(news), max_len=max(lens))
+
+
 @pytest.mark.parametrize("new", [1, 50])
 def test_attention_far_apart_values(ss, new):
     """Logits hundreds apart, page scales up to 2^40 apart, zero scales, a query row of zeros, a large scale."""
@@ -522,7 +531,7 @@ def test_attention_records_bad_pages_and_bounds(ss, new):
     assert bool(torch.isfinite(out[new:].float()).all())
 
 
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 40, 1200])
 def test_attention_in_parts_leaves_out_a_sequence_that_breaks_a_bound(ss, new):
     """Where the key axis is split, the rows of a bad sequence are left as they were, too."""
     lens = [6000, 5000]
