@@ -1,5 +1,5 @@
 // Attention of new tokens over the 8-bit paged cache, few query rows per
-// (sequence, KV head): one warp works on 16 keys at a time.
+// (sequence, KV head): one warp works on 16 keys (heads of 64: 32) at a time.
 //
 //   x[r][j] = scale q_r . (k_j s_k) log2(e),  s_k, s_v: the scales of j's page
 //   o_r = sum_j 2^(x[r][j]) (v_j s_v) / sum_j 2^(x[r][j]),  lse_r = ln 2 log2 sum_j 2^(x[r][j])
@@ -75,14 +75,19 @@ constexpr int kRowWarps = 8;               // they take a part's 16-key groups i
 constexpr int kRows = 8;                   // of a tile: the MMA's N
 
 template <int D> struct RowShape {
-    static constexpr int kRing = D == 128 ? 3 : 6;
+    static constexpr int kRing = 3;
+    // Groups of 16 keys a warp takes at a time. Two share the wait, the vote and the
+    // maxima: 64 sequences of 8192 keys, E4M3, heads of 64 take 105 us, one by one 116.
+    // Heads of 128 have no registers for two.
+    static constexpr int kTogether = D == 128 ? 1 : 2;
     static constexpr uint32_t kBox = 16 * D;      // 16 keys of K or of V
     static constexpr uint32_t kGroup = 2 * kBox;
+    static constexpr uint32_t kSlot = kTogether * kGroup;
     static constexpr int kPerSm = 2;
     // afterwards the boxes hold the warps' sums [warp][row][D + 4]
     static constexpr uint32_t kSums = kRowWarps * kRows * (D + 4) * 4;
     static constexpr uint32_t kTiles =
-        kRowWarps * kRing * kGroup > kSums ? kRowWarps * kRing * kGroup : kSums;
+        kRowWarps * kRing * kSlot > kSums ? kRowWarps * kRing * kSlot : kSums;
     static constexpr size_t kSmem = 1024 + kTiles + 2 * kRowWarps * kRows * 4 + kRowWarps * kRing * 8;
 };
 
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
                           const KvAttendParams p)
 {
     using S = RowShape<D>;
-    constexpr int ROWS = kRows, MT = D / 16, WARPS = kRowWarps, RING = S::kRing;
+    constexpr int ROWS = kRows, MT = D / 16, WARPS = kRowWarps, RING = S::kRing, U = S::kTogether;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     uint8_t *gen = smem_raw + (base - smem_u32(smem_raw));
@@ -156,9 +161,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
     if (ke > last)
         ke = last;
 
-    // this warp's groups: keys kb + 16 (warp + WARPS i)
-    const int all = ke > kb ? static_cast<int>((ke - kb + 15) / 16) : 0;
-    const int groups = all > warp ? (all - warp + WARPS - 1) / WARPS : 0;
+    // this warp's rounds of U groups: keys kb + 16 U (warp + WARPS r) on; the last
+    // round's second group may lie behind ke
+    const int all = ke > kb ? static_cast<int>((ke - kb + 16 * U - 1) / (16 * U)) : 0;
+    const int rounds = all > warp ? (all - warp + WARPS - 1) / WARPS : 0;
     if (lane == 0) {
         for (int i = 0; i < RING; ++i)
             mbar_init(&full[i], 1);
@@ -168,16 +174,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
     __syncwarp();
     bool failed = false;
     const int32_t *table = p.batch.table + s * p.batch.table_ld;
-    const uint32_t ring = base + warp * (RING * S::kGroup);
-    auto key_of = [&](int i) { return static_cast<int32_t>(kb) + 16 * (warp + WARPS * i); };
+    const uint32_t ring = base + warp * (RING * S::kSlot);
+    auto key_of = [&](int i) {
+        return static_cast<int32_t>(kb) + 16 * (U * (warp + WARPS * (i / U)) + i % U);
+    };
+    auto there = [&](int i) { return i < U * rounds && key_of(i) < ke; };
 
     // 32 groups at a time: lane i holds the page and scales of group 32 n + i;
     // the next 32 pages are loaded meanwhile. -1: outside the cache, no keys.
-    auto load_id = [&](int i) {
-        if (i >= groups)
-            return -1;
-        return __ldg(table + (key_of(i) >> p.cache.log2_page));
-    };
+    auto load_id = [&](int i) { return there(i) ? __ldg(table + (key_of(i) >> p.cache.log2_page)) : -1; };
     int32_t id = load_id(lane), id_next = load_id(32 + lane);
     float s_k, s_v, s_inv;
     auto load_scales = [&] {
@@ -190,32 +195,43 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
         if (!on)
             id = -1;
     };
-    // Copies of group i (of this warp), on page `page`, into a slot.
-    auto fetch = [&](int i, int slot, int32_t page) {
+    // Copies of round r's groups, on pages `page`, into a slot.
+    auto fetch = [&](int r, int slot, const int32_t (&page)[U]) {
         if (lane == 0) {
             uint64_t *bar = &full[slot];
-            if (page < 0) {
+            int on = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                on += page[u] >= 0;
+            if (on == 0) {
                 mbar_arrive(bar);
             } else {
-                const int32_t row =
-                    ((page * p.cache.kv_heads + h) << p.cache.log2_page) + (key_of(i) & (p.cache.page - 1));
-                const uint32_t at = ring + slot * S::kGroup;
-                mbar_arrive_expect_tx(bar, S::kGroup);
-                tc::tma_box(at, &map_k, 0, row, bar);
-                tc::tma_box(at + S::kBox, &map_v, 0, row, bar);
+                mbar_arrive_expect_tx(bar, on * S::kGroup);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (page[u] >= 0) {
+                        const int32_t row = ((page[u] * p.cache.kv_heads + h) << p.cache.log2_page) +
+                                            (key_of(U * r + u) & (p.cache.page - 1));
+                        const uint32_t at = ring + slot * S::kSlot + u * S::kGroup;
+                        tc::tma_box(at, &map_k, 0, row, bar);
+                        tc::tma_box(at + S::kBox, &map_v, 0, row, bar);
+                    }
             }
         }
     };
     {
-        const bool bad = lane < groups && (id < 0 || id >= p.cache.pages);
-        if (bad)
+        if (there(lane) && (id < 0 || id >= p.cache.pages)) {
             atomicCAS(p.err, 0, kErrPage);
-        const int32_t page = bad || lane >= groups ? -1 : id;
+            id = -1;
+        }
 #pragma unroll
-        for (int i = 0; i < RING; ++i) {
-            const int32_t at = __shfl_sync(kFull, page, i);
-            if (i < groups)
-                fetch(i, i, at);
+        for (int r = 0; r < RING; ++r) {
+            int32_t page[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                page[u] = __shfl_sync(kFull, id, U * r + u);
+            if (r < rounds)
+                fetch(r, r, page);
         }
     }
     load_scales();
@@ -268,62 +284,83 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
     float o[MT][4] = {};
     float m[2] = {-1e30f, -1e30f}, l[2] = {0.0f, 0.0f};
 
-    int slot = 0, phase = 0, i = 0;
-    for (; i < groups; ++i) {
-        if (i > 0 && (i & 31) == 0) {
+    int slot = 0, phase = 0, r = 0;
+    for (; r < rounds; ++r) {
+        const int first_group = U * r;
+        if (r > 0 && (first_group & 31) == 0) {
             id = id_next;
-            if (i + lane < groups && (id < 0 || id >= p.cache.pages))
+            if (there(first_group + lane) && (id < 0 || id >= p.cache.pages))
                 atomicCAS(p.err, 0, kErrPage);
             load_scales();
-            id_next = load_id(i + 32 + lane);
+            id_next = load_id(first_group + 32 + lane);
         }
-        const int32_t page = __shfl_sync(kFull, id, i & 31);
-        const float ks_i = __shfl_sync(kFull, s_k, i & 31), lsv = __shfl_sync(kFull, s_v, i & 31),
-                    inv = __shfl_sync(kFull, s_inv, i & 31);
+        int32_t page[U];
+        float ks_u[U], lsv[U], inv[U];
+        bool some = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int from = (first_group & 31) + u;
+            page[u] = __shfl_sync(kFull, id, from);
+            ks_u[u] = __shfl_sync(kFull, s_k, from);
+            lsv[u] = __shfl_sync(kFull, s_v, from);
+            inv[u] = __shfl_sync(kFull, s_inv, from);
+            some |= page[u] >= 0;
+        }
         if (!tc::wait_warp(&full[slot], phase, p.wait_limit_ns)) {
             failed = true;
             break;
         }
-        const int32_t key = key_of(i);
-        const uint32_t k_at = ring + slot * S::kGroup, v_at = k_at + S::kBox;
-        if (page >= 0) {
-            // two chains of products, even and odd steps
-            float sc[4] = {}, sd[4] = {};
-            uint4 wa, wb;
+        const uint32_t at = ring + slot * S::kSlot;
+        if (some) {
+            float sc[U][4] = {};
+            const int32_t key = key_of(first_group);
+            bool edge = key + 16 * U > ke || key + 16 * U > low, above = false;
 #pragma unroll
-            for (int ks = 0; ks < MT; ++ks) {
-                if ((ks & 3) == 0) {
-                    wa = lds16(k_at + box_chunk<D>(g, (D / 64) * q + ks / 4));
-                    wb = lds16(k_at + box_chunk<D>(g + 8, (D / 64) * q + ks / 4));
+            for (int u = 0; u < U; ++u) {
+                // two chains of products, even and odd steps
+                float sd[4] = {};
+                uint4 wa, wb;
+                const uint32_t k_at = at + u * S::kGroup;
+                edge |= page[u] < 0;
+#pragma unroll
+                for (int ks = 0; ks < MT; ++ks) {
+                    if ((ks & 3) == 0) {
+                        wa = lds16(k_at + box_chunk<D>(g, (D / 64) * q + ks / 4));
+                        wb = lds16(k_at + box_chunk<D>(g + 8, (D / 64) * q + ks / 4));
+                    }
+                    const uint32_t a = (ks & 3) == 0 ? wa.x : (ks & 3) == 1 ? wa.y : (ks & 3) == 2 ? wa.z : wa.w;
+                    const uint32_t c = (ks & 3) == 0 ? wb.x : (ks & 3) == 1 ? wb.y : (ks & 3) == 2 ? wb.z : wb.w;
+                    uint32_t a0, a1, a2, a3;
+                    codes4_to_f16<FP8>(a, a0, a2);
+                    codes4_to_f16<FP8>(c, a1, a3);
+                    mma_f16((ks & 1) ? sd : sc[u], a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
                 }
-                const uint32_t a = (ks & 3) == 0 ? wa.x : (ks & 3) == 1 ? wa.y : (ks & 3) == 2 ? wa.z : wa.w;
-                const uint32_t c = (ks & 3) == 0 ? wb.x : (ks & 3) == 1 ? wb.y : (ks & 3) == 2 ? wb.z : wb.w;
-                uint32_t a0, a1, a2, a3;
-                codes4_to_f16<FP8>(a, a0, a2);
-                codes4_to_f16<FP8>(c, a1, a3);
-                mma_f16((ks & 1) ? sd : sc, a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sc[u][i] = fmaf(sc[u][i] + sd[i], ks_u[u] * fac[i & 1], lsv[u]);
             }
             // sc: (key g, rows 2q, 2q + 1), (key g + 8, the same rows)
-            const bool edge = key + 16 > ke || key + 16 > low;
-            bool above = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sc[i] = fmaf(sc[i] + sd[i], ks_i * fac[i & 1], lsv);
-                if (edge) {
-                    const int32_t j = key + g + 8 * (i >> 1);
-                    if (j >= limit[i & 1] || j >= ke)
-                        sc[i] = -INFINITY;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (edge) {
+                        const int32_t j = key + 16 * u + g + 8 * (i >> 1);
+                        if (page[u] < 0 || j >= limit[i & 1] || j >= ke)
+                            sc[u][i] = -INFINITY;
+                    }
+                    above |= sc[u][i] > m[i & 1] + 8.0f;
                 }
-                above |= sc[i] > m[i & 1] + 8.0f;
-            }
             if (__any_sync(kFull, above)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float x = fmaxf(sc[i], sc[i + 2]);
+                    float x = m[i];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        x = fmaxf(x, fmaxf(sc[u][i], sc[u][i + 2]));
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-                    x = fmaxf(x, m[i]);
                     const float f = exp2_approx(m[i] - x);
                     m[i] = x;
                     l[i] *= f;
@@ -334,58 +371,70 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
                     }
                 }
             }
-            uint32_t pf[2];
-            float w[4];
+            uint32_t pf[U][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = exp2_approx(sc[i] - m[i & 1]);
-            l[0] = fmaf(w[0] + w[2], inv, l[0]);
-            l[1] = fmaf(w[1] + w[3], inv, l[1]);
-            pf[0] = transpose8x8(pack_f16(w[0], w[1]));
-            pf[1] = transpose8x8(pack_f16(w[2], w[3]));
-            // of V, lane (g, q) takes the D / 8 bytes at g D / 8 of keys 2q, 2q + 1, 2q + 8, 2q + 9
-            uint32_t v[4][D / 32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 2 * q + (i & 1) + 8 * (i >> 1);
-                if constexpr (D == 128) {
-                    const uint4 w = lds16(v_at + box_chunk<D>(r, g));
-                    v[i][0] = w.x, v[i][1] = w.y, v[i][2] = w.z, v[i][3] = w.w;
-                } else {
-                    const uint2 w = lds8(v_at + box_chunk<D>(r, g >> 1) + 8 * (g & 1));
-                    v[i][0] = w.x, v[i][1] = w.y;
-                }
-            }
-            if (FP8 && key + 16 > ke) {
-                // slots behind the last token may hold NaN codes
+            for (int u = 0; u < U; ++u) {
+                float w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (key + 2 * q + (i & 1) + 8 * (i >> 1) >= ke)
-#pragma unroll
-                        for (int w = 0; w < D / 32; ++w)
-                            v[i][w] = 0;
+                    w[i] = exp2_approx(sc[u][i] - m[i & 1]);
+                l[0] = fmaf(w[0] + w[2], inv[u], l[0]);
+                l[1] = fmaf(w[1] + w[3], inv[u], l[1]);
+                pf[u][0] = transpose8x8(pack_f16(w[0], w[1]));
+                pf[u][1] = transpose8x8(pack_f16(w[2], w[3]));
             }
-            // m tile mt: rows g, g + 8 are elements g D / 8 + 2 mt, + 1
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                uint32_t lo[4], hi[4];
-                pairs4_to_f16<FP8>(v[0][w], v[1][w], lo);
-                pairs4_to_f16<FP8>(v[2][w], v[3][w], hi);
-                mma_f16(o[2 * w], lo[0], lo[1], hi[0], hi[1], pf[0], pf[1]);
-                mma_f16(o[2 * w + 1], lo[2], lo[3], hi[2], hi[3], pf[0], pf[1]);
+            for (int u = 0; u < U; ++u) {
+                const uint32_t v_at = at + u * S::kGroup + S::kBox;
+                // of V, lane (g, q) takes the D / 8 bytes at g D / 8 of keys 2q, 2q + 1, 2q + 8, 2q + 9
+                uint32_t v[4][D / 32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 2 * q + (i & 1) + 8 * (i >> 1);
+                    if constexpr (D == 128) {
+                        const uint4 w = lds16(v_at + box_chunk<D>(r, g));
+                        v[i][0] = w.x, v[i][1] = w.y, v[i][2] = w.z, v[i][3] = w.w;
+                    } else {
+                        const uint2 w = lds8(v_at + box_chunk<D>(r, g >> 1) + 8 * (g & 1));
+                        v[i][0] = w.x, v[i][1] = w.y;
+                    }
+                }
+                if (page[u] < 0 || (FP8 && key + 16 * u + 16 > ke)) {
+                    // slots behind the last token may hold NaN codes, and a group without a page
+                    // what its place in the ring held before
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (page[u] < 0 || key + 16 * u + 2 * q + (i & 1) + 8 * (i >> 1) >= ke)
+#pragma unroll
+                            for (int w = 0; w < D / 32; ++w)
+                                v[i][w] = 0;
+                }
+                // m tile mt: rows g, g + 8 are elements g D / 8 + 2 mt, + 1
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    uint32_t lo[4], hi[4];
+                    pairs4_to_f16<FP8>(v[0][w], v[1][w], lo);
+                    pairs4_to_f16<FP8>(v[2][w], v[3][w], hi);
+                    mma_f16(o[2 * w], lo[0], lo[1], hi[0], hi[1], pf[u][0], pf[u][1]);
+                    mma_f16(o[2 * w + 1], lo[2], lo[3], hi[2], hi[3], pf[u][0], pf[u][1]);
+                }
             }
         }
-        // every lane has read the slot: the group RING on takes it
-        const int n = i + RING;
-        const int32_t page_n = __shfl_sync(kFull, (n ^ i) & ~31 ? id_next : id, n & 31);
-        if (n < groups)
-            fetch(n, slot, page_n < p.cache.pages ? page_n : -1);
+        // every lane has read the slot: the round RING on takes it
+        const int n = U * (r + RING);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t id_n = __shfl_sync(kFull, (n ^ first_group) & ~31 ? id_next : id, (n & 31) + u);
+            page[u] = id_n < p.cache.pages ? id_n : -1;
+        }
+        if (r + RING < rounds)
+            fetch(r + RING, slot, page);
         if (++slot == RING)
             slot = 0, phase ^= 1;
     }
     // a wait that ran out: the copies on their way land before the CTA exits
     if (failed)
-        for (int n = i + RING; i < n && i < groups; ++i) {
+        for (int n = r + RING; r < n && r < rounds; ++r) {
             (void)tc::wait(&full[slot], phase, p.wait_limit_ns / 8);
             if (++slot == RING)
                 slot = 0, phase ^= 1;
