@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
         constexpr int CPR[2] = {D / 16, S::kVCols / 16};
         constexpr int RPW[2] = {32 / CPR[0], 32 / CPR[1]};
         constexpr int GROUPS = S::kKRows / RPW[0]; // the same for V
-        constexpr int ITERS = (GROUPS + kConvWarps - 1) / kConvWarps;
+        constexpr int ITERS = PAIR ? (GROUPS + kConvWarps - 1) / kConvWarps : GROUPS / 4;
+        static_assert(PAIR || GROUPS % 8 == 0, "groups for four and for eight warps");
         constexpr int AHEAD = S::kRaw / 2;
         static_assert(kKeys / RPW[1] == GROUPS, "K and V items have one size");
         const int cw = warp - 10;
@@ -398,8 +399,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
         const int32_t *table = p.batch.table + s * p.batch.table_ld;
         const uint32_t raw = skv + RING * S::kStage + 16 * lane;
         const int32_t end = static_cast<int32_t>(ke), begin = static_cast<int32_t>(kb);
-        // This warp's group in an iteration; beyond the last group there is none.
-        auto group = [&](int it) { return it * kConvWarps + cw; };
+        // This warp's group in an iteration; beyond the last group there is none. A pair's
+        // warps take equal shares. A single CTA converts twice as much per step: every
+        // scheduler of the SM takes a quarter, two with one of these warps, two with two
+        // (240 rows over 16 x 8192 keys, heads of 128: 157 us, in equal shares 166; 480
+        // rows in pairs 278 and 274).
+        const int sch = warp & 3;
+        const int stride = PAIR ? kConvWarps : sch < 2 ? 4 : 8, start = PAIR ? cw : sch + (warp >= 14 ? 4 : 0);
+        auto group = [&](int it) { return it * stride + start; };
         // Items come in the order K0, K1, V0, K2, V1, ...: when V of a step is there,
         // K of the next is too, and the issuing lane waits once for both.
         auto raw_at = [&](int j, int kv) {
@@ -446,13 +453,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 for (int it = 0; it < ITERS; ++it) {
                     // the key's place in the step
                     const int32_t at = (kv == 0 ? static_cast<int32_t>(rank) * S::kKRows : 0) + group(it) * RPW[kv] + kr[kv];
-                    const int32_t first_row = __shfl_sync(kFull, kv == 0 ? row : row_before, (at >> 4) & 7);
+                    if (group(it) >= GROUPS)
+                        break;
+                    const int32_t first_row = __shfl_sync(kFull, kv == 0 ? row : row_before, at >> 4);
                     const bool on = first_row >= 0 && begin + j * kKeys + at < end;
-                    if (group(it) < GROUPS)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_at(j, kv) + group(it) * 512),
-                                     "l"(on ? codes + static_cast<int64_t>(first_row + (at & 15)) * D
-                                            : static_cast<const uint8_t *>(p.q.x)), // nothing is read there
-                                     "r"(on ? 16 : 0));
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_at(j, kv) + group(it) * 512),
+                                 "l"(on ? codes + static_cast<int64_t>(first_row + (at & 15)) * D
+                                        : static_cast<const uint8_t *>(p.q.x)), // nothing is read there
+                                 "r"(on ? 16 : 0));
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
