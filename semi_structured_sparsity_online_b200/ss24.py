@@ -480,6 +480,7 @@ def sparse_gemm_fp8(a, b, y=None, ws=None, stream=None):
 # already current and ask for the stream's raw handle only.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _same_device(index, *tensors):
@@ -495,7 +496,7 @@ def _enqueue(index, stream, name, *args):
         raise ValueError(f"{name} needs CUDA tensors")
     raw = _raw_stream(index) if stream is None else stream.cuda_stream
     fn = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -541,7 +542,7 @@ def gemm_int8(a, b, dtype=torch.bfloat16, y=None, ws=None, stream=None):
     if y is None:
         if dtype is not torch.bfloat16 and dtype is not torch.float32:
             raise TypeError("y must be bfloat16 or float32")
-        y, ld = torch.empty((m, n), dtype=dtype, device=av.device), n
+        y, ld = av.new_empty((m, n), dtype=dtype), n
     else:
         if y.dtype is not torch.bfloat16 and y.dtype is not torch.float32:
             raise TypeError("y must be bfloat16 or float32")
@@ -552,10 +553,11 @@ def gemm_int8(a, b, dtype=torch.bfloat16, y=None, ws=None, stream=None):
     _same_device(index, sa, bv, sb, y)
     ws = _workspace(ws, av)
     _enqueue(index, stream, "ss24_gemm_int8", av.data_ptr(), sa.data_ptr(), bv.data_ptr(), sb.data_ptr(), m, n, k,
-             y.data_ptr(), F32 if y.dtype is torch.float32 else BF16, ld, ws.ptr, ws.nbytes)
+             y.data_ptr(), F32 if y.dtype is torch.float32 else BF16, ld, ws.tensor.data_ptr(), ws.nbytes)
     return y
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _KV_DTYPE = {"int": (torch.int8, FMT_INT), "fp8": (torch.uint8, FMT_FP8)}
 
 
@@ -572,17 +574,17 @@ def kv_cache(pages, kv_heads, head_dim, page=64, fmt="int", device=None):
 
 
 def _kv_cache(cache) -> KvCache:
-    k, v, ks, vs, fmt = cache["k"], cache["v"], cache["k_scales"], cache["v_scales"], cache["fmt"]
-    if fmt not in _KV_DTYPE:
+    k, v, ks, vs = cache["k"], cache["v"], cache["k_scales"], cache["v_scales"]
+    dt, kind = _KV_DTYPE.get(cache["fmt"], (None, None))
+    if dt is None:
         raise ValueError("the cache's format is 'int' (8 bits) or 'fp8'")
-    dt, kind = _KV_DTYPE[fmt]
-    shape = k.shape
+    shape, scales = k.shape, ks.shape
     if (k.dtype is not dt or v.dtype is not dt or len(shape) != 4 or v.shape != shape or not k.is_contiguous()
             or not v.is_contiguous()):
         raise ValueError(f"the cache's codes must be contiguous {dt} [pages, kv_heads, page, head_dim]")
     pages, heads, page, d = shape
-    if (ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or ks.shape != (pages, heads)
-            or vs.shape != (pages, heads) or not ks.is_contiguous() or not vs.is_contiguous()):
+    if (ks.dtype is not _F32 or vs.dtype is not _F32 or scales != (pages, heads) or vs.shape != scales
+            or not ks.is_contiguous() or not vs.is_contiguous()):
         raise ValueError("the cache's scales must be contiguous float32 [pages, kv_heads]")
     if page != cache["page"]:
         raise ValueError("the cache's page is not its codes' third dimension")
@@ -591,16 +593,17 @@ def _kv_cache(cache) -> KvCache:
 
 
 def _kv_batch(cache, tokens, page_table, starts, lengths, max_new, max_len) -> KvBatch:
-    seqs = lengths.numel()
-    if (lengths.dtype is not torch.int32 or lengths.dim() != 1 or not lengths.is_contiguous()):
+    if lengths.dtype is not _I32 or lengths.dim() != 1 or not lengths.is_contiguous():
         raise ValueError("lengths must be int32 [seqs]")
-    if starts.dtype is not torch.int32 or starts.shape != (seqs + 1,) or not starts.is_contiguous():
+    seqs = lengths.numel()
+    if starts.dtype is not _I32 or starts.dim() != 1 or starts.numel() != seqs + 1 or not starts.is_contiguous():
         raise ValueError(f"starts must be int32 [{seqs + 1}]")
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != seqs:
+    if page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.shape[0] != seqs:
         raise ValueError(f"page_table must be int32 [{seqs}, most pages]")
     width = page_table.shape[1]
-    row, col = page_table.stride()
-    ld = row if seqs > 1 else width
+    ld, col = page_table.stride()
+    if seqs <= 1:
+        ld = width
     if (width > 1 and col != 1) or ld < width:
         raise ValueError("page_table must have contiguous rows")
     _same_device(cache["k"].get_device(), page_table, starts, lengths)
@@ -613,15 +616,18 @@ def _kv_batch(cache, tokens, page_table, starts, lengths, max_new, max_len) -> K
 
 
 def _head_rows(x, name, head_dim) -> HeadRows:
-    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+    dt = x.dtype
+    if dt is not _BF16 and dt is not _F32:
         raise TypeError(f"{name} must be bfloat16 or float32")
-    if x.dim() != 3 or x.shape[2] != head_dim or x.stride(2) != 1:
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, {head_dim}] with contiguous rows")
+    tokens, heads, d = x.shape
+    ts, hs, es = x.stride()
+    if d != head_dim or es != 1:
         raise ValueError(f"{name} must be [tokens, heads, {head_dim}] with contiguous rows")
     # a stride that only one row would use is free
-    tokens, heads, _ = x.shape
-    ts, hs, _ = x.stride()
-    return HeadRows(x.data_ptr(), BF16 if x.dtype is torch.bfloat16 else F32, heads,
-                    ts if tokens > 1 else heads * head_dim, hs if heads > 1 else head_dim)
+    return HeadRows(x.data_ptr(), BF16 if dt is _BF16 else F32, heads, ts if tokens > 1 else heads * head_dim,
+                    hs if heads > 1 else head_dim)
 
 
 def kv_append(cache, k, v, page_table, starts, lengths, max_new=None, max_len=None, ws=None, stream=None):
@@ -638,7 +644,7 @@ def kv_append(cache, k, v, page_table, starts, lengths, max_new=None, max_len=No
     index = cache["k"].get_device()
     _same_device(index, k, v)
     ws = _workspace(ws, k)
-    _enqueue(index, stream, "ss24_kv_append", c, b, kr, vr, ws.ptr, ws.nbytes)
+    _enqueue(index, stream, "ss24_kv_append", c, b, kr, vr, ws.tensor.data_ptr(), ws.nbytes)
     return cache
 
 
@@ -658,6 +664,8 @@ def kv_attention(q, cache, page_table, starts, lengths, scale=None, causal=True,
     qr = _head_rows(q, "q", d)
     b = _kv_batch(cache, q.shape[0], page_table, starts, lengths, max_new, max_len)
     heads = qr.heads
+    index = cache["k"].get_device()
+    _same_device(index, q)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         outr = HeadRows(out.data_ptr(), qr.dtype, heads, heads * d, d)
@@ -665,20 +673,21 @@ def kv_attention(q, cache, page_table, starts, lengths, scale=None, causal=True,
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
         outr = _head_rows(out, "out", d)
+        _same_device(index, out)
     if lse is True:
-        lse = q.new_empty((b.tokens, heads), dtype=torch.float32)
+        lse = q.new_empty((b.tokens, heads), dtype=_F32)
     elif lse is False or lse is None:
         lse = None
-    elif lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous float32 [tokens, q_heads]")
-    index = cache["k"].get_device()
-    _same_device(index, q, out, lse)
+    else:
+        if lse.dtype is not _F32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous float32 [tokens, q_heads]")
+        _same_device(index, lse)
     ws = _workspace(ws, q)
-    n = lib().ss24_kv_attention_scratch_bytes(c, b, heads)
+    n = (_lib or lib()).ss24_kv_attention_scratch_bytes(c, b, heads)
     scratch = q.new_empty(n, dtype=torch.uint8) if n > 0 else None
     _enqueue(index, None, "ss24_kv_attention", qr, c, b, d ** -0.5 if scale is None else float(scale),
              1 if causal else 0, outr, None if lse is None else lse.data_ptr(),
-             None if scratch is None else scratch.data_ptr(), max(n, 0), ws.ptr, ws.nbytes)
+             None if scratch is None else scratch.data_ptr(), n if n > 0 else 0, ws.tensor.data_ptr(), ws.nbytes)
     return out if lse is None else (out, lse)
 
 
