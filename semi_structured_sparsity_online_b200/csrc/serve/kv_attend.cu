@@ -678,8 +678,10 @@ cudaError_t launch(K kern, int64_t grid, int threads, size_t smem, cudaStream_t 
 }
 
 // Up to 32 rows per (sequence, KV head) go to the kernel above, more to the
-// tensor-memory kernel in tiles of 256 (16 sequences of up to 8192 keys, 8 KV heads
-// of 128: 32 rows 86 and 145 us, 96 rows 151 and 137).
+// tensor-memory kernel, whose time hardly depends on the rows up to 256. 32 rows
+// here and 40 there, INT8 heads of 128: 16 sequences of 1024 to 8192 keys 87 and 137
+// us, 32 of up to 1000 keys 17 and 22; 16 sequences of 8192 keys 175 and 139, one
+// of 30000 47 and 40.
 bool wide(const KvAttendParams &p) { return p.batch.max_new * p.group > 32; }
 
 template <int D, bool FP8> cudaError_t launch_rows(const KvAttendParams &p, cudaStream_t stream)
