@@ -33,7 +33,7 @@
 // Measured: a prompt of 8192 tokens, 32 heads of 128 on 8 KV heads, INT8, pages of
 // 64: 550 - 565 us, 1.0 PFLOP/s (0.61 of the measured peak), tensor pipe 48% and
 // special-function unit 48% active. 4 x up to 509 tokens over up to 4000 keys, 28
-// heads of 64 on 4, E4M3, pages of 16: 83 us, special functions 52%.
+// heads of 64 on 4, E4M3, pages of 16: 82 us, special functions 52%.
 #include "kv_attend.cuh"
 #include "tcgen05.cuh"
 
@@ -158,10 +158,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             mbar_init(&bars->kv_empty[i], two ? 2 : 1); // from the issuing warps
         }
         for (int i = 0; i < 2; ++i) {
+            // warps that have rows of row tile i
+            const int warps = (live - 128 * CTAS * i + 31) / 32;
             mbar_init(&bars->q_full[i], CTAS * 4);
             for (int half = 0; half < 2; ++half) {
                 mbar_init(&bars->s_full[i][half], 1);
-                mbar_init(&bars->p_full[i][half], CTAS * 4);
+                mbar_init(&bars->p_full[i][half], warps < 1 ? 1 : warps < 4 * CTAS ? warps : 4 * CTAS);
             }
             mbar_init(&bars->o_full[i], 1);
         }
@@ -198,7 +200,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
         if (w == 0 || two) {
             const bool on = row < live;
             const RowAt a = row_at(p, row0 + (on ? row : 0), h, first, count, len);
-            const int32_t limit = on ? a.limit : 0;
+            // a row behind the tile's last needs no mask: nothing reads its result (40
+            // rows over 16 x 8192 keys, heads of 64: 86 us; masked in every step, and with
+            // the warps that have no row at work, 114)
+            const int32_t limit = on ? a.limit : INT32_MAX;
+            // a warp without rows leaves S as its weights, and is not waited for
+            const int halves = __any_sync(kFull, on) ? 2 * steps : 0;
             float fac = 0.0f;
             {
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q.x) +
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             auto factor = [&](float s_k) { return fmaxf(s_k * fac, 0x1p-126f); };
             constexpr int GS = COARSE ? 32 : 16, GN = 64 / GS; // keys that share scales, such groups
             float m = -1e30f, l = 0.0f;
-            for (int i = 0; i < 2 * steps; ++i) {
+            for (int i = 0; i < halves; ++i) {
                 const int j = i >> 1, half = i & 1;
                 // a lane that gives up says so in the vote below
                 const bool late = !tc::wait(&bars->s_full[w][half], j & 1, p.wait_limit_ns);
