@@ -97,32 +97,6 @@ template <int D> __device__ __forceinline__ uint32_t box_chunk(int r, int c)
     return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Sequences in order of falling length (equal ones by number), so that the CTAs
-// of a long one do not start last: 64 sequences between 1024 and 8192 tokens take
-// 98 us instead of 120. One thread counts for one sequence; more of them than
-// threads even out without.
-// `room`: shared memory for a number per thread.
-__device__ __forceinline__ int32_t longest_first(const KvBatch &b, uint32_t rank, int32_t *room)
-{
-    const int n = static_cast<int>(b.seqs), tid = threadIdx.x;
-    if (n == 1 || n > static_cast<int>(blockDim.x))
-        return rank;
-    const int32_t mine = tid < n ? __ldg(b.lengths + tid) : -1;
-    room[tid] = mine;
-    __syncthreads();
-    uint32_t before = 0;
-    if (tid < n)
-        for (int i = 0; i < n; ++i)
-            before += room[i] > mine || (room[i] == mine && i < tid);
-    __syncthreads();
-    if (tid < n && before == rank)
-        room[0] = tid;
-    __syncthreads();
-    const int32_t s = room[0];
-    __syncthreads();
-    return s;
-}
-
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
     kv_attend_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -679,9 +653,9 @@ cudaError_t launch(K kern, int64_t grid, int threads, size_t smem, cudaStream_t 
 
 // Up to 32 rows per (sequence, KV head) go to the kernel above, more to the
 // tensor-memory kernel, whose time hardly depends on the rows up to 256. 32 rows
-// here and 40 there, INT8 heads of 128: 16 sequences of 1024 to 8192 keys 87 and 137
-// us, 32 of up to 1000 keys 17 and 22; 16 sequences of 8192 keys 175 and 139, one
-// of 30000 47 and 40.
+// here and 40 there, INT8 heads of 128: 16 sequences of 1024 to 8192 keys 88 and 127
+// us, 32 of up to 1000 keys 17 and 22; 16 sequences of 8192 keys 175 and 129, one
+// of 30000 47 and 38.
 bool wide(const KvAttendParams &p) { return p.batch.max_new * p.group > 32; }
 
 template <int D, bool FP8> cudaError_t launch_rows(const KvAttendParams &p, cudaStream_t stream)

@@ -133,8 +133,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
     const int h = b % p.cache.kv_heads;
     b /= p.cache.kv_heads;
     // the last row tiles see the most keys: they start first
-    const int64_t tile = p.row_tiles - 1 - b % p.row_tiles, s = b / p.row_tiles;
+    const int64_t tile = p.row_tiles - 1 - b % p.row_tiles;
     grid_dependency_wait();
+    // where the CTAs are more than the SMs
+    const int64_t s = gridDim.x > 148 ? longest_first(p.batch, b / p.row_tiles, reinterpret_cast<int32_t *>(gen))
+                                      : b / p.row_tiles;
 
     int32_t first, count, len;
     const bool known = kv_sequence(p.batch, s, p.err, &first, &count, &len);
