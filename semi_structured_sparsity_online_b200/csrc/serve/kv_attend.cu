@@ -17,10 +17,9 @@
 // below 2^-24 of that magnitude.
 //
 // The weights of the second product carry the V scale: w = 2^(x + log2 s_v -
-// M) with M a running bound on x + log2 s_v, so that w <= 2^8 fits fp16
-// (rounded once, 2^-11 relative) and its small values are small next to the
-// sum they enter. M moves only when a value exceeds it by 2^8. The denominator
-// sums w / s_v in binary32. Scales s_v below 2^-100 count as 2^-100.
+// M), rounded once to fp16, with a reference point M that follows the keys at
+// hand (kv_attend.cuh). The denominator sums w / s_v in binary32. Scales s_v
+// below 2^-100 count as 2^-100.
 //
 // Bound by memory where there is enough of it: 64 sequences of 1024 to 8192 keys,
 // 8 KV heads of 128, INT8: 98 - 102 us, 5.8 TB/s (0.88 of the measured copy);
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
         s_k = on ? __ldg(p.cache.scales[0] + ph) : 0.0f;
         const float v = on ? fmaxf(__ldg(p.cache.scales[1] + ph), 0x1p-100f) : 1.0f;
         s_v = log2f(v);
-        s_inv = __frcp_rn(v);
+        s_inv = __frcp_rn(v) * kWeightUnit;
         if (!on)
             id = -1;
     };
@@ -257,6 +256,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
 
     float o[MT][4] = {};
     float m[2] = {-1e30f, -1e30f}, l[2] = {0.0f, 0.0f};
+    // the highest m of each row, until the warps' sums are joined
+    if (g == 0)
+        sm_m[warp][2 * q] = sm_m[warp][2 * q + 1] = -1e30f;
+    __syncwarp();
 
     int slot = 0, phase = 0, r = 0;
     for (; r < rounds; ++r) {
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
         if (some) {
             float sc[U][4] = {};
             const int32_t key = key_of(first_group);
-            bool edge = key + 16 * U > ke || key + 16 * U > low, above = false;
+            bool edge = key + 16 * U > ke || key + 16 * U > low, off = false;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 // two chains of products, even and odd steps
@@ -314,35 +317,50 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
                     sc[u][i] = fmaf(sc[u][i] + sd[i], ks_u[u] * fac[i & 1], lsv[u]);
             }
             // sc: (key g, rows 2q, 2q + 1), (key g + 8, the same rows)
+            if (edge)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (edge) {
+                    for (int i = 0; i < 4; ++i) {
                         const int32_t j = key + 16 * u + g + 8 * (i >> 1);
                         if (page[u] < 0 || j >= limit[i & 1] || j >= ke)
                             sc[u][i] = -INFINITY;
                     }
-                    above |= sc[u][i] > m[i & 1] + 8.0f;
-                }
-            if (__any_sync(kFull, above)) {
+            float most[2]; // of this lane's keys
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                most[i] = fmaxf(sc[0][i], sc[0][i + 2]);
+#pragma unroll
+                for (int u = 1; u < U; ++u)
+                    most[i] = fmaxf(most[i], fmaxf(sc[u][i], sc[u][i + 2]));
+                off |= most[i] - m[i] > kWeightMost || most[i] - m[i] < kWeightLeast;
+            }
+            if (__any_sync(kFull, off)) {
+                const bool may_fall = __all_sync(kFull, fmaxf(l[0], l[1]) < kFallBelow);
+                float to[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float x = m[i];
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        x = fmaxf(x, fmaxf(sc[u][i], sc[u][i + 2]));
+                    float x = most[i];
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-                    const float f = exp2_approx(m[i] - x);
-                    m[i] = x;
-                    l[i] *= f;
+                    to[i] = weight_reference(m[i], x, sm_m[warp][2 * q + i], may_fall);
+                }
+                if (__any_sync(kFull, to[0] != m[0] || to[1] != m[1])) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        o[mt][i] *= f;
-                        o[mt][i + 2] *= f;
+                    for (int i = 0; i < 2; ++i) {
+                        const float f = exp2_approx(m[i] - to[i]);
+                        m[i] = to[i];
+                        l[i] *= f;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            o[mt][i] *= f;
+                            o[mt][i + 2] *= f;
+                        }
+                        if (g == 0)
+                            sm_m[warp][2 * q + i] = fmaxf(sm_m[warp][2 * q + i], to[i]);
                     }
+                    __syncwarp();
                 }
             }
             uint32_t pf[U][2];
@@ -449,9 +467,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
             acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
         }
         const bool any = den > 0.0f;
-        const float inv = any ? __frcp_rn(den) : 0.0f;
+        const float inv = any ? weight_inverse(den) : 0.0f;
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        const float lse2 = any ? top + log2f(den) : -INFINITY;
+        const float lse2 = any ? top + kWeightUnitLog + log2f(den) : -INFINITY;
         const RowAt a = row_at(p, row0 + r, h, first, count, len);
         const int64_t flat = a.token * (static_cast<int64_t>(p.cache.kv_heads) * p.group) + a.head;
         if (p.splits > 1) {

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     uint8_t *gen = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t sq = base, skv = base + 2 * S::kQ;
-    float4 *scales = reinterpret_cast<float4 *>(gen + S::kTiles); // [][8]: s_k, log2 s_v, 1 / s_v
+    float4 *scales = reinterpret_cast<float4 *>(gen + S::kTiles); // [][8]: s_k, log2 s_v, 2^-7 / s_v
     Bars *bars = reinterpret_cast<Bars *>(scales + S::kScaleRing * 8);
     uint32_t *tmem_base = reinterpret_cast<uint32_t *>(bars + 1);
 
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             // never 0 (a page of zero keys, scale 0): 0 times a masked -infinity is NaN
             auto factor = [&](float s_k) { return fmaxf(s_k * fac, 0x1p-126f); };
             constexpr int GS = COARSE ? 32 : 16, GN = 64 / GS; // keys that share scales, such groups
-            float m = -1e30f, l = 0.0f;
+            float m = -1e30f, top = -1e30f, l = 0.0f;
             for (int i = 0; i < halves; ++i) {
                 const int j = i >> 1, half = i & 1;
                 // a lane that gives up says so in the vote below
@@ -285,13 +285,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                     x = max3(__float_as_uint(x), y[GS - 2], y[GS - 1]);
                     mx = fmaxf(mx, fmaf(fmaxf(x, z), f[g].x, f[g].y));
                 }
-                if (__any_sync(kFull, late || mx > m + 8.0f)) {
+                const float mn = weight_reference(m, mx, top, l < kFallBelow);
+                if (__any_sync(kFull, late || mn != m)) {
                     if (__any_sync(kFull, late)) {
                         failed = true;
                         break;
                     }
-                    const float mn = fmaxf(m, mx), scale = exp2_approx(m - mn);
+                    const float scale = exp2_approx(m - mn);
                     m = mn;
+                    top = fmaxf(top, mn);
                     l *= scale;
                     if (i > 0) {
                         // the half before: its products are done when the S behind them is (or,
@@ -340,8 +342,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 failed = true;
             tc::fence_after();
             const bool any = steps > 0 && l > 0.0f;
-            const float inv = any ? __frcp_rn(l) : 0.0f;
-            const float lse2 = any ? m + log2f(l) : -INFINITY;
+            const float inv = any ? weight_inverse(l) : 0.0f;
+            const float lse2 = any ? m + kWeightUnitLog + log2f(l) : -INFINITY;
             const int64_t flat = a.token * (static_cast<int64_t>(p.cache.kv_heads) * p.group) + a.head;
             if (!failed) {
 #pragma unroll 1
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                 const float sv = fmaxf(s_v, 0x1p-100f);
                 scales[((j - 1) % S::kScaleRing) * 8 + lane] =
                     s_v < 0.0f ? make_float4(0.0f, -INFINITY, 0.0f, 0.0f)
-                               : make_float4(s_k, log2f(sv), __frcp_rn(sv), 0.0f);
+                               : make_float4(s_k, log2f(sv), __frcp_rn(sv) * kWeightUnit, 0.0f);
             }
             const int32_t key = begin + j * kKeys + 16 * lane;
             const bool there = lane < 8 && key < end, on = there && id >= 0 && id < p.cache.pages;
