@@ -630,11 +630,11 @@ int64_t ss24_kv_attention_scratch_bytes(const ss24_kv_cache *cache, const ss24_k
  * 16-byte aligned, any contents, this call's own until it has run. q is taken
  * with 11 significant bits below its row's largest magnitude (bf16 has 8), the
  * products are summed in binary32. The weights e^{z_j} s_v enter the second
- * product in fp16: each is off by at most 2^-11 of itself or 2^-16 of the
- * largest among up to 128 neighbouring keys, and weights below 2^-65 of the row's
- * largest are lost; the sum of weights does not round them. V scales below
- * 2^-100 count as 2^-100. Cache codes of the tokens seen must be finite; others
- * are not used. Error word: 15 (a wait ran
+ * product in fp16: for V scales of 2^-40 or more each is off by at most 2^-11 of
+ * itself or 2^-16 of the largest among up to 128 neighbouring keys, and weights
+ * below 2^-65 of the row's largest are lost; the sum of weights does not round
+ * them. V scales below 2^-100 count as 2^-100. Cache codes of the tokens seen
+ * must be finite; others are not used. Error word: 15 (a wait ran
  * out), 16, 17. Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT,
  * SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_ARG (scale not finite, causal),
  * SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */

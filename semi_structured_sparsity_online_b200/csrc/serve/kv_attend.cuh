@@ -50,14 +50,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 // A move costs the accumulators a pass, so M leaves room for what comes: 10 bits above a y
 // that rose, 9 bits below one that fell. A prompt of 8192 tokens, 32 heads of 128, logits
 // of deviation 1.2, 3.5 and 9: 551, 598 and 899 us (with M only rising, 8 bits at a time,
-// 553, 584 and 706; 3 bits above and 24 below one that rose: 551, 710 and 899).
-// M stays within 2^40 of the highest it was and does not fall where the sum of weights is
-// large (tiny V scales), which keeps both sums in binary32's range; weights are then lost
-// below 2^-65 of the largest.
+// 553, 584 and 706; 5 bits above and 19 below one that rose: 551, 710 and 899).
+// M stays within 2^40 of the highest it was, and where the sum of weights over the V scales
+// has reached 2^80 (scales below 2^-40) it does not fall: after a fall by 40 it is at most
+// 2^120, what follows adds 2^15 2^-7 2^100 a key, so that 2^17 keys stay in binary32's
+// range. Weights are lost below 2^-65 of the largest.
 constexpr float kWeightMost = 15.0f, kWeightLeast = -9.0f; // y - M that M stays at
 constexpr float kWeightRisen = 5.0f, kWeightFallen = 0.0f; // y - M after a move
 constexpr float kWeightFall = 40.0f;
-constexpr float kFallBelow = 0x1p60f; // the sum of weights that M may still fall with
+constexpr float kFallBelow = 0x1p80f; // the sum of weights that M may still fall with
 // The sum of weights over the V scales is taken in units of 2^kWeightUnitLog.
 constexpr float kWeightUnitLog = 7.0f, kWeightUnit = 0x1p-7f;
 // M for keys whose largest exponent is y (-infinity: none); `top`: the highest M yet.

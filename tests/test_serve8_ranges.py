@@ -83,6 +83,8 @@ def test_a_sink_without_a_value(ss, fmt, d, page, heads, new, keys, mass):  # no
     q = torch.randn(new, heads, d, generator=gen(2), device="cuda") * 0.3
     q[..., 0] = math.log(keys * mass / (1 - mass)) * d**0.5 / (127 / 50 if fmt == "int" else 448 / 200)
     compare(ss, layer, q.bfloat16(), keys, 2.0**-30, range(d))
+    layer.cache["v_scales"].fill_(2.0**-40)
+    compare(ss, layer, q.bfloat16(), keys, 2.0**-30, range(d))
 
 
 @pytest.mark.parametrize("d,page,heads,new", FORMS)
