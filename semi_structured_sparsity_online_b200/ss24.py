@@ -516,7 +516,9 @@ def _workspace(ws, t):
 
 
 def _int8_rows(d, name):
-    """Codes and scales of an INT8 operand with one scale per row."""
+    """Codes and scales of a dense INT8 operand with one scale per row."""
+    if d.get("meta") is not None:
+        raise ValueError(f"{name} must be dense: it has the metadata of a sparse pass")
     v, s = d["values"], d["scales"]
     if v.dtype != torch.int8 or v.dim() != 2 or not v.is_contiguous():
         raise ValueError(f"{name}['values'] must be contiguous int8 [rows, k]")
