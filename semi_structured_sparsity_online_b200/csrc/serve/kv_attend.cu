@@ -234,9 +234,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
         }
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-        // 2^-e with e the exponent of amax, kept to normal numbers
-        int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-        e = e < -100 ? -100 : e > 100 ? 100 : e;
+        const int e = query_exponent(static_cast<int>(__float_as_uint(amax) >> 23) - 127);
         const float down = exp2_int(-e);
 #pragma unroll
         for (int ks = 0; ks < MT; ++ks) {

@@ -75,6 +75,11 @@ __device__ __forceinline__ float weight_inverse(float sum)
     return sum > 1.0f ? __frcp_rn(sum) * kWeightUnit : __frcp_rn(sum * 0x1p7f);
 }
 
+// The power of two by which a row of q is brought into fp16, from the exponent of its
+// largest magnitude. At most 112, so that 2^112 times the softmax scale stays finite: bf16's
+// largest value is then 65280 in fp16. At least -120, for the same product's sake.
+__device__ __forceinline__ int query_exponent(int e) { return e < -120 ? -120 : e > 112 ? 112 : e; }
+
 // Row r of a (sequence, KV head): its token row, its query head, and the keys
 // it sees.
 struct RowAt {

@@ -220,8 +220,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                     top = max(top, max(max(v.x & 0x7fff, (v.x >> 16) & 0x7fff), max(v.y & 0x7fff, (v.y >> 16) & 0x7fff)));
                     top = max(top, max(max(v.z & 0x7fff, (v.z >> 16) & 0x7fff), max(v.w & 0x7fff, (v.w >> 16) & 0x7fff)));
                 }
-                int e = static_cast<int>(top >> 7) - 127;
-                e = e < -100 ? -100 : e > 100 ? 100 : e;
+                const int e = query_exponent(static_cast<int>(top >> 7) - 127);
                 // a negative scale turns q, so that the factor of S is never negative
                 const float down = on ? copysignf(exp2_int(-e), p.scale_log2) : 0.0f;
                 fac = fabsf(p.scale_log2) * exp2_int(e);

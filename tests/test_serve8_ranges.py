@@ -8,7 +8,7 @@ import math
 import pytest
 import torch
 
-from test_serve8 import U16, UB, U32, Layer, gen, i32, ss  # noqa: F401 (ss: the fixture)
+from test_serve8 import U16, UB, U32, Layer, check_attention, gen, i32, ss  # noqa: F401 (ss: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -155,3 +155,24 @@ def test_tiny_and_huge_value_scales(ss, d, page, heads, new):  # noqa: F811
         one = ss.kv_attention(q, layer.cache, layer.table([keys]), i32([0, new]), i32([keys]), max_new=new, max_len=keys)
         assert bool(torch.isfinite(out.float()).all())
         assert float((out.double() / scale - one.double()).norm() / one.double().norm()) <= 2 * UB
+
+
+@pytest.mark.parametrize("fmt", ["int", "fp8"])
+@pytest.mark.parametrize("d,page,heads,new", FORMS)
+@pytest.mark.parametrize("bits", [125, 118, 113, -113, -119])
+def test_queries_of_any_magnitude(ss, fmt, d, page, heads, new, bits):  # noqa: F811
+    """Finite queries up to bf16's largest and down to its smallest normal ones, on K scales that bring the logits back
+    to order 1."""
+    keys = 300
+    layer = Layer(ss, fmt, d, page, 1, keys, 1, seed=10).fill([keys], 10)
+    layer.cache["k_scales"].mul_(2.0**-bits)
+    q = torch.randn(new, heads, d, generator=gen(11), device="cuda").clamp_(-7, 7)
+    q = (q * 2.0**(bits - (bits == 125))).bfloat16()
+    if bits == 125:
+        q[0, 0, 0] = torch.finfo(torch.bfloat16).max
+    assert bool(torch.isfinite(q).all())
+    ws = ss.Workspace()
+    out, lse = ss.kv_attention(q, layer.cache, layer.table([keys]), i32([0, new]), i32([keys]), max_new=new, max_len=keys,
+                               lse=True, ws=ws)
+    assert ws.error() == 0
+    check_attention(layer, q, out, lse, [0, new], [keys], True, d**-0.5)
