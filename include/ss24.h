@@ -624,7 +624,7 @@ int64_t ss24_kv_attention_scratch_bytes(const ss24_kv_cache *cache, const ss24_k
  *   z_j = scale q . k_j;  out = sum_j e^{z_j} v_j / sum_j e^{z_j};
  *   lse = log(sum_j e^{z_j})
  * with k_j, v_j the values the codes stand for. A row that sees no key gets
- * out 0 and lse -infinity. out: bf16, q_heads; lse: fp32 [tokens][q_heads] or
+ * out 0 and lse -infinity; a row with a NaN in q gets NaN. out: bf16, q_heads; lse: fp32 [tokens][q_heads] or
  * NULL. Rows of q outside starts[0] .. starts[seqs] - 1 are left as they were
  * in out and lse. scratch: device, ss24_kv_attention_scratch_bytes() bytes,
  * 16-byte aligned, any contents, this call's own until it has run. q is taken

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
             acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
             acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
         }
-        const bool any = den > 0.0f;
+        const bool any = den != 0.0f; // NaN from a NaN in q
         const float inv = any ? weight_inverse(den) : 0.0f;
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         const float lse2 = any ? top + kWeightUnitLog + log2f(den) : -INFINITY;
@@ -530,7 +530,6 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) kv_attend_jo
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w)
         top = fmaxf(top, part_top[w]);
-    const bool any = top > -INFINITY;
     constexpr int PER = D / 32;
     float acc[PER] = {};
     float den = 0.0f;
@@ -538,7 +537,7 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) kv_attend_jo
 #pragma unroll 4
     for (int i = warp; i < p.splits; i += kJoinWarps) {
         // a part without keys for the row has weight 0 and finite sums (zeros)
-        const float w = any ? exp2_approx(weight[i] - top) : 0.0f;
+        const float w = weight[i] == -INFINITY ? 0.0f : exp2_approx(weight[i] - top);
         float x[PER];
         if constexpr (PER == 4)
             *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(src + static_cast<int64_t>(i) * D);
@@ -564,12 +563,12 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) kv_attend_jo
         r.x += sums[w][2 * tid], r.y += sums[w][2 * tid + 1];
         den += part_den[w];
     }
-    const float inv = den > 0.0f ? __frcp_rn(den) : 0.0f;
+    const float inv = den != 0.0f ? __frcp_rn(den) : 0.0f;
     __nv_bfloat16 *dst =
         static_cast<__nv_bfloat16 *>(p.out.x) + token * p.out.token_ld + head * p.out.head_ld + 2 * tid;
     *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(r.x * inv, r.y * inv);
     if (p.lse && tid == 0)
-        p.lse[flat] = den > 0.0f ? kLn2 * (top + log2f(den)) : -INFINITY;
+        p.lse[flat] = den != 0.0f ? kLn2 * (top + log2f(den)) : -INFINITY;
 }
 
 // The same for few parts of many rows, where a CTA per row would be mostly start: a
@@ -614,8 +613,7 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) kv_attend_jo
         for (int o = kFewParts / 2; o; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
         top = __shfl_sync(kFull, top, 0);
-        const bool any = top > -INFINITY;
-        const float w = any ? exp2_approx(lse - top) : 0.0f; // 0 for a part without keys
+        const float w = lse == -INFINITY ? 0.0f : exp2_approx(lse - top); // 0 for a part without keys
         float den = 0.0f, acc[PER] = {};
 #pragma unroll
         for (int i = 0; i < kFewParts; ++i)
@@ -626,6 +624,7 @@ template <int D> __global__ void __launch_bounds__(kJoinWarps * 32) kv_attend_jo
                 for (int j = 0; j < PER; ++j)
                     acc[j] = fmaf(wi, x[i][j], acc[j]);
             }
+        const bool any = den != 0.0f;
         const float inv = any ? __frcp_rn(den) : 0.0f;
         __nv_bfloat16 *dst =
             static_cast<__nv_bfloat16 *>(p.out.x) + token * p.out.token_ld + head * p.out.head_ld + lane * PER;

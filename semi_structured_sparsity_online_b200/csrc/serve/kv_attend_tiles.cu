@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             if (!failed && steps > 0 && !tc::wait_warp(&bars->o_full[w], 0, p.wait_limit_ns))
                 failed = true;
             tc::fence_after();
-            const bool any = steps > 0 && l > 0.0f;
+            const bool any = steps > 0 && l != 0.0f; // NaN from a NaN in q
             const float inv = any ? weight_inverse(l) : 0.0f;
             const float lse2 = any ? m + kWeightUnitLog + log2f(l) : -INFINITY;
             const int64_t flat = a.token * (static_cast<int64_t>(p.cache.kv_heads) * p.group) + a.head;

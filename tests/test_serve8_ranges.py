@@ -176,3 +176,24 @@ def test_queries_of_any_magnitude(ss, fmt, d, page, heads, new, bits):  # noqa: 
                                lse=True, ws=ws)
     assert ws.error() == 0
     check_attention(layer, q, out, lse, [0, new], [keys], True, d**-0.5)
+
+
+@pytest.mark.parametrize("fmt", ["int", "fp8"])
+@pytest.mark.parametrize("d,page,heads,new", FORMS + [(128, 64, 7, 700)])
+@pytest.mark.parametrize("keys", [200, 6000])
+def test_a_query_of_nan_shows(ss, fmt, d, page, heads, new, keys):  # noqa: F811
+    """In one part of the key axis and in several: the row's result and lse are NaN, not those of a row without keys,
+    and no other row changes."""
+    keys = max(keys, new)
+    layer = Layer(ss, fmt, d, page, 1, keys, 1, seed=12).fill([keys], 12)
+    q = torch.randn(new, heads, d, generator=gen(13), device="cuda").bfloat16()
+    where = (layer.table([keys]), i32([0, new]), i32([keys]))
+    good, good_lse = ss.kv_attention(q, layer.cache, *where, max_new=new, max_len=keys, lse=True)
+    bad = q.clone()
+    bad[new // 2, heads - 1] = math.nan
+    out, lse = ss.kv_attention(bad, layer.cache, *where, max_new=new, max_len=keys, lse=True)
+    assert bool(out[new // 2, heads - 1].isnan().all()) and bool(lse[new // 2, heads - 1].isnan())
+    out[new // 2, heads - 1], lse[new // 2, heads - 1] = good[new // 2, heads - 1], good_lse[new // 2, heads - 1]
+    # a CTA's other rows: their reference may move with a neighbour's vote, which scales by powers of two
+    assert float((out.float() - good.float()).abs().max()) <= float(good.float().abs().max()) * UB
+    assert torch.equal(lse.isfinite(), good_lse.isfinite())
