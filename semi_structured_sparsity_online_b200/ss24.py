@@ -479,8 +479,9 @@ def sparse_gemm_fp8(a, b, y=None, ws=None, stream=None):
 # microseconds: they check with few attribute reads, enter no context that is
 # already current and ask for the stream's raw handle only.
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# The private forms are faster; a build of torch without CUDA lacks them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _same_device(index, *tensors):
