@@ -211,13 +211,23 @@ class Workspace:
 
 
 _default_ws = {}
+_graph_ws = []
 
 
 def default_workspace(device=None) -> Workspace:
+    """The device's workspace for calls that name none, made by the first of them. Make it before a capture: a call
+    captured without one gets a workspace of its own, part of the graph, whose error word every replay clears."""
     dev = torch.device(device or "cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    if dev not in _default_ws:
-        _default_ws[dev] = Workspace(dev)
-    return _default_ws[dev]
+    ws = _default_ws.get(dev)
+    if ws is None:
+        ws = Workspace(dev)
+        if torch.cuda.is_current_stream_capturing():
+            _graph_ws.append(ws)  # the graph's calls use it, on whichever stream, as long as the graph lives
+            return ws
+        # calls on other streams find it cleared
+        torch.cuda.current_stream().synchronize()
+        _default_ws[dev] = ws
+    return ws
 
 
 def _alloc_outputs(x_rows, k, pattern, fmt: Format, in_dtype, device, batch=None):
