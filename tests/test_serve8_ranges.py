@@ -29,19 +29,29 @@ def key_at(layer, j):
     return int(layer.order[0, j // layer.page]), j % layer.page
 
 
-def compare(ss, layer, q, keys, unit, channels=None):  # noqa: F811
+def compare(ss, layer, q, keys, unit, channels=None, causal=False, table=None, seen=None, error=0):  # noqa: F811
     """Elements against their bound and, with `channels`, those channels' norm. unit: a small weight's absolute error
-    over the largest weight among its keys, where that weight is far above all others."""
+    over the largest weight among its keys, where that weight is far above all others. table: another page table than
+    the layer's, with which only the keys `seen` are seen and the error word is `error`."""
     new, heads, d = q.shape
     ws = ss.Workspace()
-    out, lse = ss.kv_attention(q, layer.cache, layer.table([keys]), i32([0, new]), i32([keys]), causal=False, max_new=new,
+    table = layer.table([keys]) if table is None else table
+    out, lse = ss.kv_attention(q, layer.cache, table, i32([0, new]), i32([keys]), causal=causal, max_new=new,
                                max_len=keys, lse=True, ws=ws)
-    assert ws.error() == 0
+    assert ws.error() == error
     k, v = layer.values("k", 0, keys)[:, 0], layer.values("v", 0, keys)[:, 0]
     z = q.double().view(-1, d) @ k.T * d**-0.5
-    p = torch.softmax(z, -1)
+    there = torch.ones(new, keys, dtype=torch.bool, device="cuda") if seen is None else seen.expand(new, keys)
+    if causal:
+        at = keys - new + torch.arange(new, device="cuda")
+        there = there & (torch.arange(keys, device="cuda") <= at[:, None])
+    there = there[:, None].expand(new, heads, keys).reshape(-1, keys)
+    z = z.masked_fill(~there, -math.inf)
+    none = ~there.any(1)
+    p = torch.softmax(z, -1).nan_to_num(0.0)
     ref = p @ v
     got = out.double().view(-1, d)
+    assert bool((got[none] == 0).all()) and bool((lse.view(-1)[none] == -math.inf).all())
     # Roundings. Of the result: half a bf16 step. Of a weight: half an fp16 step, 2^-11, or below 2^-14 half of fp16's
     # least step, 2^-25 of the reference 2^M. With W the largest weight among the keys taken together (at most 128
     # aligned ones) M is at most log2 W + 9: 2^-16 W, for weights below 2^-5 W. Where no key before has a larger
@@ -49,7 +59,7 @@ def compare(ss, layer, q, keys, unit, channels=None):  # noqa: F811
     page_of = torch.arange(keys, device="cuda") // layer.page
     s_v = layer.cache["v_scales"][torch.from_numpy(layer.order[0]).cuda().long()[page_of], 0].double()
     w = p * s_v
-    pad = -keys % 128
+    pad = max(-keys % 128, 256 - keys)  # two blocks at least
     block = torch.nn.functional.pad(w, (0, pad)).view(w.shape[0], -1, 128).amax(2)
     first, second = block.topk(2, 1).values.T
     alone = (block == first[:, None]) & (first > 2.0**8 * second)[:, None]
@@ -61,7 +71,8 @@ def compare(ss, layer, q, keys, unit, channels=None):  # noqa: F811
     tol = UB * ref.abs() + (p @ v.abs()) * (2 * dz + U16 + 2 * keys * U32) + floor
     assert bool(((got - ref).abs() <= tol).all()), float(((got - ref).abs() / tol).max())
     lse_ref = torch.logsumexp(z, -1)
-    assert bool(((lse.double().view(-1) - lse_ref).abs() <= (dz[:, 0] + 2 * keys * U32 + 4 * U32 * lse_ref.abs())).all())
+    off = (lse.double().view(-1) - lse_ref).abs() <= dz[:, 0] + 2 * keys * U32 + 4 * U32 * lse_ref.abs()
+    assert bool(off[~none].all())
     # A result of many small terms of both signs: bf16's rounding is at most UB of the norm, the weights' roundings are
     # independent of each other and each at most U16 of its term, so that their sum's norm is about U16 / sqrt(3) of
     # the result's; four U16 leave room for the exponents' roundings.
@@ -197,3 +208,23 @@ def test_a_query_of_nan_shows(ss, fmt, d, page, heads, new, keys):  # noqa: F811
     # a CTA's other rows: their reference may move with a neighbour's vote, which scales by powers of two
     assert float((out.float() - good.float()).abs().max()) <= float(good.float().abs().max()) * UB
     assert torch.equal(lse.isfinite(), good_lse.isfinite())
+
+
+@pytest.mark.parametrize("fmt", ["int", "fp8"])
+@pytest.mark.parametrize("d,page,heads,new", FORMS + [(128, 16, 3, 1), (64, 32, 8, 1), (128, 128, 1, 600)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_page_outside_the_cache_counts_as_no_keys(ss, fmt, d, page, heads, new, causal):  # noqa: F811
+    """First, last, neighbouring and all page numbers bad: as if their keys were masked, a row that sees no others like
+    one without keys. The unused table entries stay out of range."""
+    for keys in (max(new, 5 * page + 3), 3000):
+        pages = -(-keys // page)
+        layer = flat_layer(ss, fmt, d, page, keys, 14)
+        q = (torch.randn(new, heads, d, generator=gen(15), device="cuda") * 0.3).bfloat16()
+        for bad in ([0], [pages - 1], [1, 4], [2, 3], range(0, pages, 2), range(1, pages, 2), range(pages)):
+            bad = list(bad)
+            table = layer.table([keys])
+            table[0, bad] = torch.tensor([(layer.pages, -1, 1 << 30)[i % 3] for i in bad], dtype=torch.int32, device="cuda")
+            seen = torch.ones(pages, dtype=torch.bool, device="cuda")
+            seen[bad] = False
+            compare(ss, layer, q, keys, 2.0**-16, causal=causal, table=table, seen=seen.repeat_interleave(page)[:keys],
+                    error=16)
