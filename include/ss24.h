@@ -636,7 +636,8 @@ int64_t ss24_kv_attention_scratch_bytes(const ss24_kv_cache *cache, const ss24_k
  * them. V scales below 2^-100 count as 2^-100. Cache codes of the tokens seen
  * must be finite; others are not used. Error word: 15 (a wait ran
  * out), 16, 17. Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT,
- * SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_ARG (scale not finite, causal),
+ * SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_ARG (scale or scale * log2(e) not
+ * finite, causal),
  * SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */
 ss24_status ss24_kv_attention(const ss24_head_rows *q, const ss24_kv_cache *cache, const ss24_kv_batch *batch,
                               float scale, int32_t causal, const ss24_head_rows *out, float *lse, void *scratch,

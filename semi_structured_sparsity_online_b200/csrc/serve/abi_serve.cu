@@ -191,7 +191,8 @@ ss24_status ss24_kv_attention(const ss24_head_rows *q, const ss24_kv_cache *cach
         return st;
     if (q->heads != out->heads || q->heads % p.cache.kv_heads != 0)
         return SS24_ERR_SHAPE;
-    if (!std::isfinite(scale) || (causal != 0 && causal != 1))
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    if (!std::isfinite(p.scale_log2) || (causal != 0 && causal != 1))
         return SS24_ERR_ARG;
     if (!aligned(lse, 4))
         return SS24_ERR_ALIGN;
@@ -204,7 +205,6 @@ ss24_status ss24_kv_attention(const ss24_head_rows *q, const ss24_kv_cache *cach
     if (need > 0 && (!scratch || scratch_bytes < 4 * need || !aligned(scratch, 16)))
         return SS24_ERR_WORKSPACE;
     p.lse = lse;
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.causal = causal;
     p.part_o = static_cast<float *>(scratch);
     p.part_lse = p.part_o + need / (p.cache.d + 1) * p.cache.d;

@@ -42,3 +42,10 @@ else:
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38])
+def test_attention_refuses_a_scale_that_overflows(scale):
+    """The kernels take the scale times log2(e) in binary32."""
+    from test_serve8_host import ARG, attend
+    assert attend(scale=scale) == ARG
