@@ -606,7 +606,7 @@ typedef struct {
  * codes. The same call made again leaves the cache as it is. New tokens at a
  * negative position (more new tokens than lengths[s]) are dropped; slots behind
  * lengths[s], other pages and their scales are left as they were. Pages that
- * receive tokens belong to one sequence each. max_new and max_len 0: nothing
+ * receive tokens stand in one place of one sequence each. max_new and max_len 0: nothing
  * is launched. Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT,
  * SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */
 ss24_status ss24_kv_append(const ss24_kv_cache *cache, const ss24_kv_batch *batch, const ss24_head_rows *k,
@@ -624,20 +624,24 @@ int64_t ss24_kv_attention_scratch_bytes(const ss24_kv_cache *cache, const ss24_k
  *   z_j = scale q . k_j;  out = sum_j e^{z_j} v_j / sum_j e^{z_j};
  *   lse = log(sum_j e^{z_j})
  * with k_j, v_j the values the codes stand for. A row that sees no key gets
- * out 0 and lse -infinity; a row with a NaN in q gets NaN. out: bf16, q_heads; lse: fp32 [tokens][q_heads] or
- * NULL. Rows of q outside starts[0] .. starts[seqs] - 1 are left as they were
- * in out and lse. scratch: device, ss24_kv_attention_scratch_bytes() bytes,
- * 16-byte aligned, any contents, this call's own until it has run. q is taken
+ * out 0 and lse -infinity; a row with a NaN in q gets NaN. out: bf16, q_heads;
+ * lse: fp32 [tokens][q_heads] or NULL. Rows of q outside starts[0] ..
+ * starts[seqs] - 1 are left as they were in out and lse. scratch: device,
+ * ss24_kv_attention_scratch_bytes() bytes, 16-byte aligned, any contents, this
+ * call's own until it has run. The bounds choose the kernel (max_new times the
+ * query heads of a KV head: up to 32 rows or more) and the parts of the key axis
+ * (max_len); loose ones give the same results later: a request of 2000 keys with
+ * max_len 131072 35 us instead of 16, 64 single tokens over 4000 keys each with
+ * max_new 64 279 us instead of 115. q is taken
  * with 11 significant bits below its row's largest magnitude (bf16 has 8), the
  * products are summed in binary32. The weights e^{z_j} s_v enter the second
  * product in fp16: for V scales of 2^-40 or more each is off by at most 2^-11 of
  * itself or 2^-16 of the largest among up to 128 neighbouring keys, and weights
  * below 2^-65 of the row's largest are lost; the sum of weights does not round
  * them. V scales below 2^-100 count as 2^-100. Cache codes of the tokens seen
- * must be finite; others are not used. Error word: 15 (a wait ran
- * out), 16, 17. Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT,
- * SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_ARG (scale or scale * log2(e) not
- * finite, causal),
+ * must be finite; others are not used. Error word: 15 (a wait ran out), 16, 17.
+ * Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT, SS24_ERR_SHAPE,
+ * SS24_ERR_ALIGN, SS24_ERR_ARG (scale or scale * log2(e) not finite, causal),
  * SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */
 ss24_status ss24_kv_attention(const ss24_head_rows *q, const ss24_kv_cache *cache, const ss24_kv_batch *batch,
                               float scale, int32_t causal, const ss24_head_rows *out, float *lse, void *scratch,

@@ -667,7 +667,10 @@ def kv_attention(q, cache, page_table, starts, lengths, scale=None, causal=True,
     over the cache (ss24_kv_attention); the sequences as in kv_append. scale:
     1 / sqrt(head_dim) by default. Returns out [tokens, q_heads, head_dim]
     (bfloat16), or (out, lse) with lse=True or an lse tensor (float32 [tokens,
-    q_heads]). Tight max_new and max_len choose a better split of the work."""
+    q_heads]). max_new and max_len choose the kernel and the split of the keys, so
+    give them where the host knows them: 64 single tokens over 4000 keys each take
+    115 us with max_new=1 and 279 without, a request of 2000 keys in a page table
+    for 131072 16 us with max_len=2000 and 35 without."""
     if stream is not None and stream != torch.cuda.current_stream(stream.device):
         # what is allocated here belongs to the stream that uses it
         with torch.cuda.stream(stream):
