@@ -115,9 +115,10 @@
  *
  * Test hook. When the environment variable SS24_TEST_SKIP_TILE holds a
  * number t >= 0 at the time of a call, the first CTA of that call's
- * strided-axis kernel does not copy its t-th tile and every wait of the
- * kernel gives up after 10 ms instead of two seconds: a wait runs out on
- * purpose, and the error word shows it. For tests of that path only.
+ * strided-axis kernel, INT8 product or attention does not copy (or hand over)
+ * its t-th tile, stage, round or step of keys and every wait of the kernel
+ * gives up after 10 ms instead of two seconds: a wait runs out on purpose, and
+ * the error word shows it. For tests of that path only.
  */
 #ifndef SS24_H
 #define SS24_H

@@ -1,6 +1,7 @@
 // The C ABI of the 8-bit serving operators (include/ss24.h): host-side checks
 // and launches. Every check runs before anything is enqueued.
 #include <cmath>
+#include <cstdlib>
 
 #include "../../../include/ss24.h"
 #include "serve.cuh"
@@ -19,6 +20,20 @@ ss24_status check_ws(const void *ws, size_t ws_bytes)
 }
 
 int32_t *error_word(void *ws) { return reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kWsErrOff); }
+
+// The limit of the kernels' waits, and the test hook (ss24.h).
+void wait_limits(uint64_t *limit_ns, int32_t *skip)
+{
+    *limit_ns = kWaitLimitNs;
+    *skip = -1;
+    if (const char *t = std::getenv("SS24_TEST_SKIP_TILE")) {
+        const long v = std::strtol(t, nullptr, 10);
+        if (v >= 0 && v < INT32_MAX) {
+            *skip = static_cast<int32_t>(v);
+            *limit_ns = kTestWaitLimitNs;
+        }
+    }
+}
 
 ss24_status check_cache(const ss24_kv_cache *c, KvCache *out)
 {
@@ -125,7 +140,8 @@ ss24_status ss24_gemm_int8(const int8_t *a, const float *a_scale, const int8_t *
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) ||
         !aligned(y, y_dtype == SS24_BF16 ? 2 : 4))
         return SS24_ERR_ALIGN;
-    GemmInt8Params p{m, n, k, ldy, a, b, a_scale, b_scale, y, y_dtype == SS24_F32, error_word(ws), kWaitLimitNs};
+    GemmInt8Params p{m, n, k, ldy, a, b, a_scale, b_scale, y, y_dtype == SS24_F32, error_word(ws)};
+    wait_limits(&p.wait_limit_ns, &p.test_skip);
     return cuda_status(launch_gemm_int8(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -209,7 +225,7 @@ ss24_status ss24_kv_attention(const ss24_head_rows *q, const ss24_kv_cache *cach
     p.part_o = static_cast<float *>(scratch);
     p.part_lse = p.part_o + need / (p.cache.d + 1) * p.cache.d;
     p.err = error_word(ws);
-    p.wait_limit_ns = kWaitLimitNs;
+    wait_limits(&p.wait_limit_ns, &p.test_skip);
     return cuda_status(launch_kv_attend(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

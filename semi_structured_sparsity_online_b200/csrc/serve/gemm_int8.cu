@@ -136,7 +136,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (rank == 0)
                     mbar_arrive_expect_tx(&bars->full[it], 2 * kPairStage);
                 const uint32_t bar = tc::cluster_addr(smem_u32(&bars->full[it]), 0);
-                tc::tma_box_pair(at, &map_w, kt * kBK, row_w, bar);
+                if (issued != p.test_skip || blockIdx.x != 0)
+                    tc::tma_box_pair(at, &map_w, kt * kBK, row_w, bar);
                 tc::tma_box_pair(at + kBM * kBK, &map_x, kt * kBK, row_x, bar);
                 ++issued;
                 if (++it == kPairStages)
@@ -303,12 +304,14 @@ __global__ void __launch_bounds__(kSplitThreads)
             }
             const uint32_t at = smem_u32(stages + s * S::kStage);
             mbar_arrive_expect_tx(&full[s], S::kStage);
-            tc::tma_box(at, &map_w, kt * kBK, static_cast<int32_t>(c0), &full[s]);
+            if (issued != p.test_skip || blockIdx.x != 0)
+                tc::tma_box(at, &map_w, kt * kBK, static_cast<int32_t>(c0), &full[s]);
             tc::tma_box(at + kBM * kBK, &map_x, kt * kBK, static_cast<int32_t>(t0), &full[s]);
         }
-        if (failed) // the copies already issued land before the CTA can exit
-            for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-                (void)tc::wait(&full[i % STAGES], (i / STAGES) & 1, p.wait_limit_ns);
+        // the copies land before the CTA can exit, also where the other warp gave up on one
+        for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+            if (!tc::wait(&full[i % STAGES], (i / STAGES) & 1, p.wait_limit_ns))
+                failed = true;
     } else if (warp == 1) {
         const bool lead = lane == 0;
         constexpr uint32_t kI = i8_idesc(128, BN);

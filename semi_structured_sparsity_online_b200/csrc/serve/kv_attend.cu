@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
                 mbar_arrive_expect_tx(bar, on * S::kGroup);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (page[u] >= 0) {
+                    if (page[u] >= 0 && (r != p.test_skip || blockIdx.x != 0 || warp != 0)) {
                         const int32_t row = ((page[u] * p.cache.kv_heads + h) << p.cache.log2_page) +
                                             (key_of(U * r + u) & (p.cache.page - 1));
                         const uint32_t at = ring + slot * S::kSlot + u * S::kGroup;

@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
             }
 
             // ---- the row's output -------------------------------------------------
-            if (!failed && steps > 0 && !tc::wait_warp(&bars->o_full[w], 0, p.wait_limit_ns))
+            // also after a wait that ran out: the commit's arrival comes before the CTA exits
+            if (steps > 0 && !tc::wait_warp(&bars->o_full[w], 0, p.wait_limit_ns))
                 failed = true;
             tc::fence_after();
             const bool any = steps > 0 && l != 0.0f; // NaN from a NaN in q
@@ -527,7 +528,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                     next_rows(j + AHEAD);
                 convert(raw_at(j, kv), skv + st * S::kStage, kv);
                 tc::fence_proxy();
-                arrive(&bars->kv_full[st]);
+                if (kv == 0 || j != p.test_skip || blockIdx.x != 0 || cw != 0)
+                    arrive(&bars->kv_full[st]);
                 // the item kRaw on takes the slot
                 if (kv == 0 && j == 0)
                     fetch(AHEAD - 1, 1);

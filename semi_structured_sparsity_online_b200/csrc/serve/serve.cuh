@@ -22,6 +22,7 @@ struct GemmInt8Params {
     int32_t y_f32;
     int32_t *err;
     uint64_t wait_limit_ns;
+    int32_t test_skip; // >= 0: a stage that the first CTA does not copy (ss24.h, test hook)
 };
 
 // The paged cache: codes [pages][kv_heads][page][d], scales [pages][kv_heads].
@@ -68,6 +69,7 @@ struct KvAttendParams {
     float *part_lse;     // [tokens * q_heads][splits], base 2
     int32_t *err;
     uint64_t wait_limit_ns;
+    int32_t test_skip; // >= 0: a round or step whose keys or values the first CTA does not hand over
 };
 
 cudaError_t launch_gemm_int8(const GemmInt8Params &p, cudaStream_t stream);
