@@ -639,8 +639,9 @@ int64_t ss24_kv_attention_scratch_bytes(const ss24_kv_cache *cache, const ss24_k
  * product in fp16: for V scales of 2^-40 or more each is off by at most 2^-11 of
  * itself or 2^-16 of the largest among up to 128 neighbouring keys, and weights
  * below 2^-65 of the row's largest are lost; the sum of weights does not round
- * them. V scales below 2^-100 count as 2^-100. Cache codes of the tokens seen
- * must be finite; others are not used. Error word: 15 (a wait ran out), 16, 17.
+ * them. V scales below 2^-100 count as 2^-100. The result of a row with a z_j
+ * beyond 2^24 in magnitude, where binary32 holds no fraction, is unspecified.
+ * Cache codes of the tokens seen must be finite; others are not used. Error word: 15 (a wait ran out), 16, 17.
  * Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT, SS24_ERR_SHAPE,
  * SS24_ERR_ALIGN, SS24_ERR_ARG (scale or scale * log2(e) not finite, causal),
  * SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */
