@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
         if (some) {
             float sc[U][4] = {};
             const int32_t key = key_of(first_group);
-            bool edge = key + 16 * U > ke || key + 16 * U > low, off = false;
+            bool edge = key + 16 * U > ke || key + 16 * U > low;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 // two chains of products, even and odd steps
@@ -325,15 +325,28 @@ __global__ void __launch_bounds__(kRowWarps * 32, RowShape<D>::kPerSm)
                             sc[u][i] = -INFINITY;
                     }
             float most[2]; // of this lane's keys
+            bool off = false;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 most[i] = fmaxf(sc[0][i], sc[0][i + 2]);
 #pragma unroll
                 for (int u = 1; u < U; ++u)
                     most[i] = fmaxf(most[i], fmaxf(sc[u][i], sc[u][i + 2]));
-                off |= most[i] - m[i] > kWeightMost || most[i] - m[i] < kWeightLeast;
+                off |= weight_off(m[i], most[i]);
             }
-            if (__any_sync(kFull, off)) {
+            // The rows stay where no lane's keys are too high and a lane of each row has some
+            // that are high enough.
+            bool move = __any_sync(kFull, off);
+            if (move) {
+                const bool high = most[0] - m[0] > kWeightMost || most[1] - m[1] > kWeightMost;
+                uint32_t near0 = __ballot_sync(kFull, most[0] - m[0] >= kWeightLeast);
+                uint32_t near1 = __ballot_sync(kFull, most[1] - m[1] >= kWeightLeast);
+                near0 |= near0 >> 16, near1 |= near1 >> 16;
+                near0 |= near0 >> 8, near1 |= near1 >> 8;
+                near0 |= near0 >> 4, near1 |= near1 >> 4;
+                move = __any_sync(kFull, high) || (near0 & near1 & 15) != 15;
+            }
+            if (move) {
                 const bool may_fall = __all_sync(kFull, fmaxf(l[0], l[1]) < kFallBelow);
                 float to[2];
 #pragma unroll

@@ -49,8 +49,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 // before was larger).
 // A move costs the accumulators a pass, so M leaves room for what comes: 10 bits above a y
 // that rose, 9 bits below one that fell. A prompt of 8192 tokens, 32 heads of 128, logits
-// of deviation 1.2, 3.5 and 9: 551, 598 and 899 us (with M only rising, 8 bits at a time,
-// 553, 584 and 706; 5 bits above and 19 below one that rose: 551, 710 and 899).
+// of deviation 1.2, 3.5 and 9: 555, 604 and 890 us (with M only rising, 8 bits at a time,
+// 560, 590 and 691; 5 bits above and 19 below one that rose: 551, 710 and 899).
 // M stays within 2^40 of the highest it was, and where the sum of weights over the V scales
 // has reached 2^80 (scales below 2^-40) it does not fall: after a fall by 40 it is at most
 // 2^120, what follows adds 2^15 2^-7 2^100 a key, so that 2^17 keys stay in binary32's
@@ -61,6 +61,12 @@ constexpr float kWeightFall = 40.0f;
 constexpr float kFallBelow = 0x1p80f; // the sum of weights that M may still fall with
 // The sum of weights over the V scales is taken in units of 2^kWeightUnitLog.
 constexpr float kWeightUnitLog = 7.0f, kWeightUnit = 0x1p-7f;
+// Whether M may have to move for an exponent y (true for -infinity, too).
+__device__ __forceinline__ bool weight_off(float m, float y)
+{
+    constexpr float kMid = (kWeightMost + kWeightLeast) / 2, kHalf = (kWeightMost - kWeightLeast) / 2;
+    return fabsf(y - m - kMid) > kHalf;
+}
 // M for keys whose largest exponent is y (-infinity: none); `top`: the highest M yet.
 // Differences are compared: m + 15 would round where m is large.
 __device__ __forceinline__ float weight_reference(float m, float y, float top, bool may_fall)

@@ -284,17 +284,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tiles_kernel(const 
                     x = max3(__float_as_uint(x), y[GS - 2], y[GS - 1]);
                     mx = fmaxf(mx, fmaf(fmaxf(x, z), f[g].x, f[g].y));
                 }
-                const float mn = weight_reference(m, mx, top, l < kFallBelow);
-                if (__any_sync(kFull, late || mn != m)) {
+                if (__any_sync(kFull, late || weight_off(m, mx))) {
                     if (__any_sync(kFull, late)) {
                         failed = true;
                         break;
                     }
-                    const float scale = exp2_approx(m - mn);
+                    const float mn = weight_reference(m, mx, top, l < kFallBelow), scale = exp2_approx(m - mn);
+                    const bool moved = __any_sync(kFull, mn != m);
                     m = mn;
                     top = fmaxf(top, mn);
                     l *= scale;
-                    if (i > 0) {
+                    if (i > 0 && moved) {
                         // the half before: its products are done when the S behind them is (or,
                         // in the last step, when the barrier that stands for it says so)
                         if (!tc::wait_warp(&bars->s_full[w][half ^ 1], (j + half) & 1, p.wait_limit_ns)) {
