@@ -22,9 +22,9 @@
 // below 2^-100 count as 2^-100.
 //
 // Bound by memory where there is enough of it: 64 sequences of 1024 to 8192 keys,
-// 8 KV heads of 128, INT8: 98 - 102 us, 5.8 TB/s (0.88 of the measured copy);
-// 131072 keys, E4M3: 53 - 55 us, 5.0 TB/s. A 16-key group takes 370 instructions, a
-// third of them the conversion of the codes (ALU pipe 57% active).
+// 8 KV heads of 128, INT8: 96 - 102 us, 5.8 TB/s (0.88 of the measured copy);
+// 131072 keys, E4M3: 53 - 55 us, 5.0 TB/s. A 16-key group takes 380 instructions, a
+// third of them the conversion of the codes (ALU pipe 51% active).
 #include "kv_attend.cuh"
 #include "tcgen05.cuh"
 

@@ -31,9 +31,9 @@
 // moves by more than 2^8, which waits for the other half's products first.
 //
 // Measured: a prompt of 8192 tokens, 32 heads of 128 on 8 KV heads, INT8, pages of
-// 64: 550 - 565 us, 1.0 PFLOP/s (0.61 of the measured peak), tensor pipe 48% and
+// 64: 544 - 565 us, 1.0 PFLOP/s (0.61 of the measured peak), tensor pipe 48% and
 // special-function unit 48% active. 4 x up to 509 tokens over up to 4000 keys, 28
-// heads of 64 on 4, E4M3, pages of 16: 82 us, special functions 52%.
+// heads of 64 on 4, E4M3, pages of 16: 82 - 86 us, special functions 52%.
 #include "kv_attend.cuh"
 #include "tcgen05.cuh"
 
