@@ -607,9 +607,10 @@ typedef struct {
  * codes. The same call made again leaves the cache as it is. New tokens at a
  * negative position (more new tokens than lengths[s]) are dropped; slots behind
  * lengths[s], other pages and their scales are left as they were. Pages that
- * receive tokens stand in one place of one sequence each. max_new and max_len 0: nothing
- * is launched. Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT,
- * SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */
+ * receive tokens stand in one place of one sequence each. max_new and max_len
+ * 0: nothing is launched. Errors: SS24_ERR_NULL, SS24_ERR_DTYPE,
+ * SS24_ERR_FORMAT, SS24_ERR_SHAPE, SS24_ERR_ALIGN, SS24_ERR_WORKSPACE,
+ * SS24_ERR_CUDA. */
 ss24_status ss24_kv_append(const ss24_kv_cache *cache, const ss24_kv_batch *batch, const ss24_head_rows *k,
                            const ss24_head_rows *v, void *ws, size_t ws_bytes, ss24_stream stream);
 
@@ -640,8 +641,9 @@ int64_t ss24_kv_attention_scratch_bytes(const ss24_kv_cache *cache, const ss24_k
  * itself or 2^-16 of the largest among up to 128 neighbouring keys, and weights
  * below 2^-65 of the row's largest are lost; the sum of weights does not round
  * them. V scales below 2^-100 count as 2^-100. The result of a row with a z_j
- * beyond 2^24 in magnitude, where binary32 holds no fraction, is unspecified.
- * Cache codes of the tokens seen must be finite; others are not used. Error word: 15 (a wait ran out), 16, 17.
+ * beyond 2^23 in magnitude, where binary32 holds hardly a fraction, is
+ * unspecified. Cache codes of the tokens seen must be finite; others are not
+ * used. Error word: 15 (a wait ran out), 16, 17.
  * Errors: SS24_ERR_NULL, SS24_ERR_DTYPE, SS24_ERR_FORMAT, SS24_ERR_SHAPE,
  * SS24_ERR_ALIGN, SS24_ERR_ARG (scale or scale * log2(e) not finite, causal),
  * SS24_ERR_WORKSPACE, SS24_ERR_CUDA. */

@@ -228,3 +228,24 @@ def test_a_page_outside_the_cache_counts_as_no_keys(ss, fmt, d, page, heads, new
             seen[bad] = False
             compare(ss, layer, q, keys, 2.0**-16, causal=causal, table=table, seen=seen.repeat_interleave(page)[:keys],
                     error=16)
+
+
+@pytest.mark.parametrize("d,page,heads,new", FORMS)
+@pytest.mark.parametrize("keys", [200, 3000])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_up_to_2_to_the_23(ss, d, page, heads, new, keys, sign):  # noqa: F811
+    """Logits near +-2^23, some pages' up to 14 bits above the others', where binary32 has steps of 1: every weight stays
+    finite, so that values that are alike within a column give themselves."""
+    layer = flat_layer(ss, "int", d, page, keys, 17)
+    layer.cache["k"].fill_(100)
+    layer.cache["v"].copy_(torch.arange(d, device="cuda") - 40)
+    more = torch.randint(0, 12, layer.cache["k_scales"].shape, generator=gen(18), device="cuda")
+    layer.cache["k_scales"].copy_((1 / 50 + more.double() * (2.0**-23 / 50)).float())
+    q = torch.full((new, heads, d), float(sign), device="cuda").bfloat16()
+    z = float(d * 100 / 50 * (1 + 12 * 2.0**-23))
+    out, lse = ss.kv_attention(q, layer.cache, layer.table([keys]), i32([0, new]), i32([keys]), scale=0.999 * 2**23 / z,
+                               causal=False, max_new=new, max_len=keys, lse=True)
+    ref = (torch.arange(d, device="cuda").double() - 40) / 50
+    # the V scale 1 / 50 is rounded, a weight to 2^-11, the sums of n terms, the result
+    assert bool(((out.double() - ref).abs() <= ref.abs() * (UB + U16 + 2 * keys * U32)).all())
+    assert bool(((lse.double() / sign - 2**23).abs() <= 2**23 * 0.01).all())
